@@ -25,7 +25,11 @@ UNITS = [("lstm_kernels.hip", [])] + [
     for bf in (0, 1) for st in (0, 1) for nwv in (4, 8)
 ] + [("lstm_rec_res_inst.hip", [f"-DLSTM_RES_SHAPE={k}"]) for k in range(3)] + [("lstm_fwd.cpp", []), ("lstm_plan.cpp", []), ("lstm_fwd_noalloc.hip", []),
                  ("lstm_bwd.hip", [])] + [
-    ("lstm_bwd_res_inst.hip", [f"-DLSTM_BWD_RES_SHAPE={k}"]) for k in range(16)]
+    ("lstm_bwd_res_inst.hip", [f"-DLSTM_BWD_RES_SHAPE={k}"]) for k in range(16)] + [
+    # the decoder's attention: one unit per direction, element type and padded head size
+    (f"dec_attn_{kind}_inst.hip", [f"-DDEC_BF16={bf}", f"-DDEC_DP={dp}"])
+    for kind in ("fwd", "bwd") for bf in (0, 1) for dp in (256, 224, 192, 160, 128, 96, 64, 32)] + [
+    ("dec_attn_misc.hip", []), ("dec_api.cpp", []), ("dec_beam.hip", [])]
 PEAK_UNITS = [("lstm_peaks.hip", [])]
 BUILD_DIR = os.path.join(HERE, "_build")
 

@@ -1,0 +1,104 @@
+// Attention over encoder outputs: joining the parts of a split key axis, and
+// delta = <dout, o> of the backward pass.
+#include "dec_attn.h"
+#include "dec_attn_launch.h"
+
+namespace lstm {
+namespace {
+
+// LR lanes (a power of two, 4 columns each) join one row's parts: with m the
+// parts' largest maximum, o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i.
+template <typename T, int LR>
+__global__ void __launch_bounds__(256) attn_combine_kernel(AttnParams p) {
+  const long long row = (long long)blockIdx.x * (256 / LR) + threadIdx.x / LR;
+  const int c = (threadIdx.x % LR) * 4;
+  if (row >= (long long)p.B * p.Hkv * p.rows) return;
+  const float* ml = p.part_ml + row * p.nsplit * 2;
+  float m = -INFINITY;
+  for (int i = 0; i < p.nsplit; ++i) m = fmaxf(m, ml[2 * i]);
+  const float mu = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  const float* po = p.part_o + row * p.nsplit * p.D + c;
+  for (int i = 0; i < p.nsplit; ++i) {
+    const float w = exp2_fast(ml[2 * i] - mu);
+    l += w * ml[2 * i + 1];
+    if (c < p.D) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(po + (long long)i * p.D);
+      o += x * w;
+    }
+  }
+  const int r = (int)(row % p.rows);
+  const long long bh = row / p.rows;
+  const int b = (int)(bh / p.Hkv), t = r / p.G, hq = (int)(bh % p.Hkv) * p.G + r % p.G;
+  if (c < p.D) {
+    o *= l == 0.f ? 0.f : 1.f / l;
+    char* at = p.o + b * p.so.b + t * p.so.t + hq * p.so.h + c * AT<T>::SZ;
+    if constexpr (AT<T>::BF)
+      *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+    else
+      *reinterpret_cast<f32x4*>(at) = o;
+  }
+  if (c == 0 && p.lse) p.lse[((long long)b * p.Hq + hq) * p.Tq + t] = mu * kLn2 + logf(l);
+}
+
+template <typename T>
+hipError_t combine(const AttnParams& p, hipStream_t s) {
+  const long long rows = (long long)p.B * p.Hkv * p.rows;
+  auto go = [&](auto kernel, int lr) {
+    const long long n = (rows + 256 / lr - 1) / (256 / lr);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(256), 0, s, p);
+    return hipGetLastError();
+  };
+  if (p.D <= 32) return go(attn_combine_kernel<T, 8>, 8);
+  if (p.D <= 64) return go(attn_combine_kernel<T, 16>, 16);
+  if (p.D <= 128) return go(attn_combine_kernel<T, 32>, 32);
+  return go(attn_combine_kernel<T, 64>, 64);
+}
+
+// 16 lanes a row; rows in the order of lse.
+template <typename T>
+__global__ void __launch_bounds__(256) attn_delta_kernel(AttnParams p) {
+  constexpr int SZ = AT<T>::SZ;
+  const long long row = (long long)blockIdx.x * 16 + threadIdx.x / 16;
+  if (row >= (long long)p.B * p.Hq * p.Tq) return;
+  const int t = (int)(row % p.Tq);
+  const long long bh = row / p.Tq;
+  const int b = (int)(bh / p.Hq), h = (int)(bh % p.Hq);
+  const char* o = p.o_in + b * p.so.b + t * p.so.t + h * p.so.h;
+  const char* d = p.dout + b * p.sdo.b + t * p.sdo.t + h * p.sdo.h;
+  float sum = 0.f;
+  for (int c = (threadIdx.x & 15) * 16; c < p.D * SZ; c += 256) {
+    const uint4 x = *reinterpret_cast<const uint4*>(o + c), y = *reinterpret_cast<const uint4*>(d + c);
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (AT<T>::BF) {
+        sum = fmaf(bf16_lo(xs[j]), bf16_lo(ys[j]), sum);
+        sum = fmaf(bf16_hi(xs[j]), bf16_hi(ys[j]), sum);
+      } else {
+        sum = fmaf(__builtin_bit_cast(float, xs[j]), __builtin_bit_cast(float, ys[j]), sum);
+      }
+    }
+  }
+#pragma unroll
+  for (int o2 = 8; o2 > 0; o2 >>= 1) sum += __shfl_xor(sum, o2);
+  if ((threadIdx.x & 15) == 0) p.delta[row] = sum;
+}
+
+}  // namespace
+
+hipError_t attn_combine_launch(const AttnParams& p, bool bf16, hipStream_t s) {
+  return bf16 ? combine<uint16_t>(p, s) : combine<float>(p, s);
+}
+
+hipError_t attn_delta_launch(const AttnParams& p, bool bf16, hipStream_t s) {
+  const long long n = ((long long)p.B * p.Hq * p.Tq + 15) / 16;
+  if (bf16)
+    hipLaunchKernelGGL((attn_delta_kernel<uint16_t>), dim3((unsigned)n), dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((attn_delta_kernel<float>), dim3((unsigned)n), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace lstm
