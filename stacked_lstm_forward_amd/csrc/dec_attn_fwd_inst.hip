@@ -13,18 +13,76 @@ typedef float ET;
 #endif
 constexpr int DP = DEC_DP;
 
+// The scores x of a tile become exponentials; m, l and o follow.
+template <typename T, int DP, int QC, int KT, int NTILES>
+__device__ __forceinline__ void softmax_tile(f32x4 (&x)[KT / 16][QC], f32x4 (&o)[NTILES][QC], float (&m)[QC],
+                                             float (&l)[QC], float scale_log2) {
+#pragma unroll
+  for (int qc = 0; qc < QC; ++qc) {
+    float mx = x[0][qc][0];
+#pragma unroll
+    for (int kt = 0; kt < KT / 16; ++kt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, x[kt][qc][i]);
+    // The maximum in use stays until it is 2^8 behind: exponentials up to 2^8
+    // are as exact as those below 1, and o is rescaled for few tiles only.
+    const float mn = col_max(mx) * scale_log2;
+    if (__any(mn > m[qc] + 8.f)) {
+      const float mu = fmaxf(m[qc], mn);
+      const float alpha = mu == -INFINITY ? 1.f : exp2_fast(m[qc] - mu);
+      m[qc] = mu;
+      l[qc] *= alpha;
+#pragma unroll
+      for (int n = 0; n < NTILES; ++n) o[n][qc] *= alpha;
+    }
+    const float mu = m[qc] == -INFINITY ? 0.f : m[qc];
+    float sum = 0.f;
+#pragma unroll
+    for (int kt = 0; kt < KT / 16; ++kt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = exp2_fast(fmaf(x[kt][qc][i], scale_log2, -mu));
+        x[kt][qc][i] = e;
+        sum += e;
+      }
+    l[qc] += sum;
+  }
+}
+
+// One column group's results, to o and lse or to the parts of a split.
+template <typename T, int DP, int QC, int NTILES>
+__device__ __forceinline__ void store_rows(const AttnParams& p, int b, int hk, int bh, int split, int row0, int qc,
+                                           const f32x4 (&o)[NTILES][QC], float m, float l, int lane) {
+  const int r = row0 + qc * 16 + (lane & 15);
+  if (r >= p.rows) return;
+  if (p.nsplit > 1) {
+    const long long at = ((long long)bh * p.rows + r) * p.nsplit + split;
+    store_cols_f32<T, DP, NTILES, QC>(p.part_o + at * p.D, o, qc, p.D, lane);
+    if (lane < 16) {
+      p.part_ml[at * 2] = m;
+      p.part_ml[at * 2 + 1] = l;
+    }
+    return;
+  }
+  const int t = r / p.G, hq = hk * p.G + r % p.G;
+  store_cols<T, DP, NTILES, QC>(p.o + b * p.so.b + t * p.so.t + hq * p.so.h, o, qc, l == 0.f ? 0.f : 1.f / l, p.D,
+                                lane);
+  if (lane < 16 && p.lse)
+    p.lse[((long long)b * p.Hq + hq) * p.Tq + t] = (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
+}
+
 // Each wave owns 16*QC rows (columns of S^T), the workgroup's NW waves share
 // the KT keys of a tile in LDS.
 template <typename T, int DP, int QC, int NW, int KT>
 __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
   constexpr int SZ = AT<T>::SZ, NT = NW * 64, PB = Pitch<T, DP>::B;
   constexpr int NCH = DP * SZ / 64, VR = DP * SZ / 16;  // 16-byte pieces of a row
-  constexpr int NV = KT * VR / NT;                      // pieces per thread and tile
-  static_assert(KT * VR % NT == 0, "tile divides over the threads");
+  constexpr int NV = (KT * VR + NT - 1) / NT;           // pieces per thread and tile
   constexpr int NTILES = DP / 16;
-  __shared__ __align__(16) char sk[KT * PB];
-  __shared__ __align__(16) char sv[KT * PB];
-  __shared__ __align__(16) float sbias[KT];
+  // two buffers: a tile is written while its predecessor is read, one barrier a tile
+  __shared__ __align__(16) char skb[2][KT * PB];
+  __shared__ __align__(16) char svb[2][KT * PB];
+  __shared__ __align__(16) float sbiasb[2][KT];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int item = xcd_item(blockIdx.x, gridDim.x);
@@ -62,29 +120,41 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
     for (int n = 0; n < NTILES; ++n) o[n][qc] = (f32x4){0.f, 0.f, 0.f, 0.f};
   }
 
+  // A tile's loads are issued a tile ahead; key mask bytes come with them and are applied on the way to LDS.
   uint4 rk[NV], rv[NV];
-  float rb = 0.f;
+  uint8_t rm[NV], rb = 0;
   auto load = [&](int s) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = tid + j * NT, r = s + i / VR, c = (i % VR) * 16;
-      const bool ok = r < s1 && (!mb || mb[r]);
+      const bool ok = (KT * VR % NT == 0 || i < KT * VR) && r < s1;
+      if (mb) rm[j] = ok ? mb[r] : 0;
       rk[j] = load16(kb + r * p.sk.t, c, db, ok);
       rv[j] = load16(vb + r * p.sv.t, c, db, ok);
     }
-    if (tid < KT) rb = s + tid < s1 && (!mb || mb[s + tid]) ? 0.f : -INFINITY;
+    if (tid < KT) rb = s + tid < s1 ? (mb ? mb[s + tid] : 1) : 0;
   };
-  if (s0 < s1) load(s0);
-  for (int s = s0; s < s1; s += KT) {
-    __syncthreads();
+  auto store = [&](int buf) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = tid + j * NT, a = (i / VR) * PB + (i % VR) * 16;
-      *reinterpret_cast<uint4*>(sk + a) = rk[j];
-      *reinterpret_cast<uint4*>(sv + a) = rv[j];
+      if (KT * VR % NT == 0 || i < KT * VR) {
+        if (mb && !rm[j]) rk[j] = rv[j] = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(skb[buf] + a) = rk[j];
+        *reinterpret_cast<uint4*>(svb[buf] + a) = rv[j];
+      }
     }
-    if (tid < KT) sbias[tid] = rb;
+    if (tid < KT) sbiasb[buf][tid] = rb ? 0.f : -INFINITY;
+  };
+  if (s0 < s1) {
+    load(s0);
+    store(0);
     __syncthreads();
+  }
+  int buf = 0;
+  for (int s = s0; s < s1; s += KT, buf ^= 1) {
+    const char *sk = skb[buf], *sv = svb[buf];
+    const float* sbias = sbiasb[buf];
     if (s + KT < s1) load(s + KT);
 
     f32x4 x[KT / 16][QC];
@@ -95,52 +165,176 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
       for (int qc = 0; qc < QC; ++qc) x[kt][qc] = bias;
     }
     mma_rows<T, DP, QC, KT>(x, sk, qf, lane);
-#pragma unroll
-    for (int qc = 0; qc < QC; ++qc) {
-      float mx = -INFINITY;
-#pragma unroll
-      for (int kt = 0; kt < KT / 16; ++kt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, x[kt][qc][i]);
-      const float mn = fmaxf(m[qc], col_max(mx) * p.scale_log2);
-      const float mu = mn == -INFINITY ? 0.f : mn;
-      const float alpha = exp2_fast(m[qc] - mu);
-      m[qc] = mn;
-      float sum = 0.f;
-#pragma unroll
-      for (int kt = 0; kt < KT / 16; ++kt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float e = exp2_fast(fmaf(x[kt][qc][i], p.scale_log2, -mu));
-          x[kt][qc][i] = e;
-          sum += e;
-        }
-      l[qc] = l[qc] * alpha + sum;
-#pragma unroll
-      for (int n = 0; n < NTILES; ++n) o[n][qc] *= alpha;
-    }
+    softmax_tile<T, DP, QC, KT, NTILES>(x, o, m, l, p.scale_log2);
     mma_tr<T, DP, QC, KT, NTILES>(o, sv, x, lane);
+    if (s + KT < s1) store(buf ^ 1);
+    __syncthreads();
   }
 
 #pragma unroll
   for (int qc = 0; qc < QC; ++qc) {
-    const float lt = col_sum(l[qc]);
-    const int r = row0 + qc * 16 + (lane & 15);
-    if (r >= p.rows) continue;
-    if (p.nsplit > 1) {
-      const long long at = ((long long)bh * p.rows + r) * p.nsplit + split;
-      store_cols_f32<T, DP, NTILES, QC>(p.part_o + at * p.D, o, qc, p.D, lane);
-      if (lane < 16) {
-        p.part_ml[at * 2] = m[qc];
-        p.part_ml[at * 2 + 1] = lt;
+    store_rows<T, DP, QC, NTILES>(p, b, hk, bh, split, row0, qc, o, m[qc], col_sum(l[qc]), lane);
+  }
+}
+
+// Few rows (single tokens, beams): every wave owns all 16*QC rows and keys of its
+// own, KT at a time, so k goes straight from memory into operands and v through
+// a slice of LDS that only its wave touches: no barrier until the waves' results
+// are joined.  Bound by the reading of k and v; a tile's loads are in flight
+// while its predecessor is computed.
+template <typename T, int DP, int QC, int NW, int KT>
+__global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
+  constexpr int SZ = AT<T>::SZ, PB = Pitch<T, DP>::B;
+  constexpr int NCH = DP * SZ / 64, VR = DP * SZ / 16;
+  constexpr int NV = KT * VR / 64;
+  static_assert(KT * VR % 64 == 0, "tile divides over the wave");
+  constexpr int NTILES = DP / 16;
+  constexpr int kTiles = NW * KT * PB, kJoin = QC * 16 * (DP + 4) * 4;
+  __shared__ __align__(16) char smem[kTiles > kJoin ? kTiles : kJoin];
+  __shared__ float sm[NW][QC * 16], sl[NW][QC * 16];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l15 = lane & 15;
+  const int item = xcd_item(blockIdx.x, gridDim.x);
+  const int tile = item % p.tiles, rest = item / p.tiles;
+  const int split = rest % p.nsplit, bh = rest / p.nsplit;
+  const int b = bh / p.Hkv, hk = bh % p.Hkv;
+  const int db = p.D * SZ;
+  const int s0 = split * p.kv_per_split;
+  const int s1 = min(keys_of(p, b), s0 + p.kv_per_split);
+  const char* kb = p.k + b * p.sk.b + hk * p.sk.h;
+  const char* vb = p.v + b * p.sv.b + hk * p.sv.h;
+  const uint8_t* mb = p.key_mask ? p.key_mask + (long long)b * p.S : nullptr;
+  char* sv = smem + wave * KT * PB;
+
+  const int row0 = tile * 16 * QC;
+  uint4 qf[QC][NCH];
+#pragma unroll
+  for (int qc = 0; qc < QC; ++qc) {
+    const int r = row0 + qc * 16 + l15;
+    const bool ok = r < p.rows;
+    const int t = ok ? r / p.G : 0, gh = ok ? r % p.G : 0;
+    const char* qr = p.q + b * p.sq.b + t * p.sq.t + (hk * p.G + gh) * p.sq.h;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) qf[qc][c] = load16(qr, c * 64 + g * 16, db, ok);
+  }
+  f32x4 o[NTILES][QC];
+  float m[QC], l[QC];
+#pragma unroll
+  for (int qc = 0; qc < QC; ++qc) {
+    m[qc] = -INFINITY;
+    l[qc] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NTILES; ++n) o[n][qc] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  }
+
+  uint4 kf[KT / 16][NCH], rv[NV];
+  uint8_t mk[KT / 16], mx4[KT / 16][4], mv[NV];  // mask bytes of the k rows, the score rows, the v rows
+  auto load_k = [&](int s) {
+#pragma unroll
+    for (int kt = 0; kt < KT / 16; ++kt) {
+      const int r = s + kt * 16 + l15;
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) kf[kt][c] = load16(kb + r * p.sk.t, c * 64 + g * 16, db, r < s1);
+      if (mb) {
+        mk[kt] = r < s1 ? mb[r] : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx4[kt][i] = s + kt * 16 + 4 * g + i < s1 ? mb[s + kt * 16 + 4 * g + i] : 0;
       }
-    } else {
-      const int t = r / p.G, hq = hk * p.G + r % p.G;
-      store_cols<T, DP, NTILES, QC>(p.o + b * p.so.b + t * p.so.t + hq * p.so.h, o, qc, lt == 0.f ? 0.f : 1.f / lt,
-                                    p.D, lane);
-      if (lane < 16 && p.lse)
-        p.lse[((long long)b * p.Hq + hq) * p.Tq + t] = (m[qc] == -INFINITY ? 0.f : m[qc]) * kLn2 + logf(lt);
     }
+  };
+  auto load_v = [&](int s) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = lane + j * 64, r = s + i / VR;
+      rv[j] = load16(vb + r * p.sv.t, (i % VR) * 16, db, r < s1);
+      if (mb) mv[j] = r < s1 ? mb[r] : 0;
+    }
+  };
+  const int first = s0 + wave * KT;
+  if (first < s1) {
+    load_k(first);
+    load_v(first);
+  }
+  for (int s = first; s < s1; s += NW * KT) {
+    f32x4 x[KT / 16][QC];
+#pragma unroll
+    for (int kt = 0; kt < KT / 16; ++kt) {
+      f32x4 bias;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        bias[i] = s + kt * 16 + 4 * g + i < s1 && (!mb || mx4[kt][i]) ? 0.f : -INFINITY;
+#pragma unroll
+      for (int qc = 0; qc < QC; ++qc) x[kt][qc] = bias;
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        if (mb && !mk[kt]) kf[kt][c] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int qc = 0; qc < QC; ++qc) mma_chunk<T>(x[kt][qc], kf[kt][c], qf[qc][c]);
+      }
+    }
+    if (s + NW * KT < s1) load_k(s + NW * KT);
+    softmax_tile<T, DP, QC, KT, NTILES>(x, o, m, l, p.scale_log2);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = lane + j * 64;
+      if (mb && !mv[j]) rv[j] = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(sv + (i / VR) * PB + (i % VR) * 16) = rv[j];
+    }
+    if (s + NW * KT < s1) load_v(s + NW * KT);
+    // the wave's own LDS accesses take effect in order; only the compiler has to keep them so
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    mma_tr<T, DP, QC, KT, NTILES>(o, sv, x, lane);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+  }
+
+  // join the waves: common maximum, then the sums in wave order
+#pragma unroll
+  for (int qc = 0; qc < QC; ++qc) {
+    l[qc] = col_sum(l[qc]);
+    if (lane < 16) {
+      sm[wave][qc * 16 + lane] = m[qc];
+      sl[wave][qc * 16 + lane] = l[qc];
+    }
+  }
+  float* so = reinterpret_cast<float*>(smem);
+  __syncthreads();
+  float lt[QC];
+#pragma unroll
+  for (int qc = 0; qc < QC; ++qc) {
+    const int r = qc * 16 + l15;
+    float mt = sm[0][r];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) mt = fmaxf(mt, sm[w][r]);
+    const float mu = mt == -INFINITY ? 0.f : mt;
+    lt[qc] = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) lt[qc] += exp2_fast(sm[w][r] - mu) * sl[w][r];
+    const float by = exp2_fast(m[qc] - mu);
+    m[qc] = mt;
+#pragma unroll
+    for (int n = 0; n < NTILES; ++n) o[n][qc] *= by;
+  }
+  for (int w = NW - 1; w > 0; --w) {
+    if (wave == w) {
+#pragma unroll
+      for (int qc = 0; qc < QC; ++qc)
+#pragma unroll
+        for (int n = 0; n < NTILES; ++n) {
+          f32x4* at = reinterpret_cast<f32x4*>(so + (qc * 16 + l15) * (DP + 4) + n * 16 + g * 4);
+          *at = w == NW - 1 ? o[n][qc] : *at + o[n][qc];
+        }
+    }
+    __syncthreads();
+  }
+  if (wave != 0) return;
+#pragma unroll
+  for (int qc = 0; qc < QC; ++qc) {
+#pragma unroll
+    for (int n = 0; n < NTILES; ++n)
+      if (NW > 1) o[n][qc] += *reinterpret_cast<f32x4*>(so + (qc * 16 + l15) * (DP + 4) + n * 16 + g * 4);
+    store_rows<T, DP, QC, NTILES>(p, b, hk, bh, split, row0, qc, o, m[qc], lt[qc], lane);
   }
 }
 
@@ -151,13 +345,30 @@ hipError_t launch(const AttnParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int QC, int NW, int KT>
+hipError_t launch_step(const AttnParams& p, hipStream_t s) {
+  const long long n = (long long)p.B * p.Hkv * p.tiles * p.nsplit;
+  hipLaunchKernelGGL((attn_step_kernel<ET, DP, QC, NW, KT>), dim3((unsigned)n), dim3(NW * 64), 0, s, p);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 #define DEC_FN2(bf, dp) attn_fwd_launch_##bf##_##dp
 #define DEC_FN(bf, dp) DEC_FN2(bf, dp)
 hipError_t DEC_FN(DEC_BF16, DEC_DP)(const AttnParams& p, hipStream_t s) {
-  constexpr int QC = DEC_BF16 ? 2 : 1;
-  return launch<QC, 4, DEC_BF16 ? 64 : 32>(p, s);
+  constexpr bool BF = DEC_BF16;
+  constexpr int KT = fwd_key_tile(BF, DP), QC = fwd_columns(BF);
+  switch (fwd_waves(BF, DP, p.rows)) {
+    case 0:
+      if constexpr (step_max_columns(BF, DP) == 2)
+        if (step_columns(BF, DP, p.rows) == 2) return launch_step<2, 4, BF ? 32 : 16>(p, s);
+      return launch_step<1, 4, BF ? 32 : 16>(p, s);
+    case 4: return launch<QC, 4, KT>(p, s);
+    default:
+      if constexpr (fwd_max_waves(BF, DP) == 8) return launch<QC, 8, KT>(p, s);
+      return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace lstm

@@ -24,10 +24,26 @@ DEC_ATTN_DECLARE(256)
 hipError_t attn_combine_launch(const AttnParams&, bool bf16, hipStream_t);
 hipError_t attn_delta_launch(const AttnParams&, bool bf16, hipStream_t);
 
-// Rows a forward workgroup owns, keys a backward workgroup owns and rows its
-// query-side part owns (the kernels' tile shapes).
-constexpr int fwd_rows_per_block(bool bf16) { return bf16 ? 128 : 64; }
-constexpr int fwd_key_tile(bool bf16) { return bf16 ? 64 : 32; }
+// The forward kernels' tile shapes, by rule on type, head size and rows.
+// Waves of a workgroup with rows of their own: 0 selects the kernel whose waves
+// own keys (up to 32 rows, one or two column groups).
+constexpr int fwd_columns(bool bf16) { return bf16 ? 2 : 1; }
+constexpr int fwd_key_tile(bool bf16, int dp) { return bf16 && dp <= 160 ? 64 : 32; }
+// eight waves share a tile where their operands and sums fit 256 registers a lane
+constexpr int fwd_max_waves(bool bf16, int dp) { return bf16 && dp > 160 ? 4 : 8; }
+constexpr int fwd_waves(bool bf16, int dp, int rows) {
+  return rows <= 32 ? 0 : rows <= 64 * fwd_columns(bf16) ? 4 : fwd_max_waves(bf16, dp);
+}
+// column groups of the few-rows kernel: two where they fit the registers
+constexpr int step_max_columns(bool bf16, int dp) { return dp <= (bf16 ? 192 : 128) ? 2 : 1; }
+constexpr int step_columns(bool bf16, int dp, int rows) { return rows <= 16 ? 1 : step_max_columns(bf16, dp); }
+constexpr int fwd_rows_per_block(bool bf16, int dp, int rows) {
+  return rows <= 32 ? 16 * step_columns(bf16, dp, rows) : fwd_waves(bf16, dp, rows) * 16 * fwd_columns(bf16);
+}
+// keys below which a workgroup of a split is not worth its launch
+constexpr int fwd_keys_per_block(bool bf16, int dp, int rows) {
+  return rows <= 32 ? (bf16 ? 128 : 64) : fwd_key_tile(bf16, dp);
+}
 // 16-column groups of a backward wave: two where operands and sums of that many fit the registers
 constexpr int bwd_columns(bool bf16, int dp) { return bf16 && dp <= 128 ? 2 : 1; }
 
