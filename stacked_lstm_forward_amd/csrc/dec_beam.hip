@@ -3,13 +3,14 @@
 //   rows   one wave per part of a beam's row of logits: reads it once, keeps the
 //          part's sum of exponentials and, per lane, the best value seen with the
 //          first 16-byte vector that holds it; then takes the part's K best in
-//          the order (value falling, index rising).  The k-th best of a part lies
-//          in a lane whose best is among the K best lanes', so each extraction
-//          rereads one lane's vectors only (64 at most, one per lane).
+//          the order (value falling, index rising).  These lie in the K lanes
+//          whose best come first in that order, and none is below the last of
+//          the K lanes' bests: the wave rereads these lanes' vectors only and
+//          keeps what reaches that value.
 //   join   one sentence per workgroup (several where the states are large, each
-//          joining again): log-sum-exp of every beam in 64 bits, the K best of
-//          every beam from its parts, the K best of all by rank, and the copy of
-//          the chosen states.
+//          joining again): a wave per beam takes its log-sum-exp in 64 bits and
+//          its K best from its parts, one wave the K best of all by rank, and all
+//          copy the chosen states.
 //
 // The order of every sum and every comparison is by index in the row, never by
 // address: beams with equal rows get equal sums, and their ties stay ties.
@@ -105,37 +106,63 @@ typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
 template <bool BF>
-struct Row {
-  static constexpr int VE = BF ? 8 : 4;
-  // values i .. i+VE-1 of a row of n; past its end `pad`
-  static __device__ __forceinline__ void load(const void* base, int i, int n, float pad, float (&x)[VE]) {
-    if (i + VE <= n) {
-      if constexpr (BF) {
-        const u32x4_a2 u = *reinterpret_cast<const u32x4_a2*>(static_cast<const uint16_t*>(base) + i);
+struct Row;
+template <>
+struct Row<true> {
+  static constexpr int VE = 8;
+  typedef uint16_t E;
+  typedef u32x4_a2 Raw;
+  static __device__ __forceinline__ float value(E e) { return __builtin_bit_cast(float, (uint32_t)e << 16); }
+  static __device__ __forceinline__ void split(const Raw& u, float (&x)[VE]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[2 * j] = __builtin_bit_cast(float, (uint32_t)u[j] << 16);
-          x[2 * j + 1] = __builtin_bit_cast(float, (uint32_t)u[j] & 0xffff0000u);
-        }
-      } else {
-        const u32x4_a4 u = *reinterpret_cast<const u32x4_a4*>(static_cast<const float*>(base) + i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = __builtin_bit_cast(float, (uint32_t)u[j]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        x[j] = pad;
-        if (i + j < n) {
-          if constexpr (BF)
-            x[j] = __builtin_bit_cast(float, (uint32_t) static_cast<const uint16_t*>(base)[i + j] << 16);
-          else
-            x[j] = static_cast<const float*>(base)[i + j];
-        }
-      }
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w = u[j];
+      x[2 * j] = __builtin_bit_cast(float, w << 16);
+      x[2 * j + 1] = __builtin_bit_cast(float, w & 0xffff0000u);
     }
   }
+  static __device__ __forceinline__ Raw raw(const void* base, int i) {
+    return *reinterpret_cast<const Raw*>(static_cast<const E*>(base) + i);
+  }
+  static __device__ __forceinline__ void load(const void* base, int i, int n, float pad, float (&x)[VE]);
 };
+template <>
+struct Row<false> {
+  static constexpr int VE = 4;
+  typedef float E;
+  typedef u32x4_a4 Raw;
+  static __device__ __forceinline__ float value(E e) { return e; }
+  static __device__ __forceinline__ void split(const Raw& u, float (&x)[VE]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w = u[j];
+      x[j] = __builtin_bit_cast(float, w);
+    }
+  }
+  static __device__ __forceinline__ Raw raw(const void* base, int i) {
+    return *reinterpret_cast<const Raw*>(static_cast<const E*>(base) + i);
+  }
+  static __device__ __forceinline__ void load(const void* base, int i, int n, float pad, float (&x)[VE]);
+};
+// values i .. i+VE-1 of a row of n; past its end `pad`
+template <typename R>
+__device__ __forceinline__ void load_row(const void* base, int i, int n, float pad, float (&x)[R::VE]) {
+  if (i + R::VE <= n) {
+    R::split(R::raw(base, i), x);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < R::VE; ++j) {
+    x[j] = pad;
+    if (i + j < n) x[j] = R::value(static_cast<const typename R::E*>(base)[i + j]);
+  }
+}
+__device__ __forceinline__ void Row<true>::load(const void* base, int i, int n, float pad, float (&x)[VE]) {
+  load_row<Row<true>>(base, i, n, pad, x);
+}
+__device__ __forceinline__ void Row<false>::load(const void* base, int i, int n, float pad, float (&x)[VE]) {
+  load_row<Row<false>>(base, i, n, pad, x);
+}
 
 // log2(e) as a sum of two floats
 constexpr float kL2eHi = 1.44268798828125f;
@@ -146,53 +173,17 @@ constexpr float kLowest = -3.402823466e38f;
 // reference value X that the lane has seen, summed over one vector in fp32 and
 // beyond that in 64 bits.  X follows the maximum only when that is 16 ahead, so
 // nearly never after the first vector.
+constexpr int kAhead = 4;   // vectors in flight per lane
+constexpr int kKept = 64;   // values kept by a part's second look
+
+// The K best of a part when more than kKept values reach the bound (long runs of
+// equal logits): extracted one by one, each from the lane whose next value comes
+// first, whose vectors (64 at most, one per lane) are reread.
 template <bool BF>
-__global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
+__device__ __noinline__ void part_best_by_one(const BeamParams& p, const char* base, int v0, int v1, float best,
+                                              int at, long long out) {
   constexpr int VE = Row<BF>::VE;
   const int lane = threadIdx.x & 63;
-  const long long job = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int row = (int)(job / p.parts), part = (int)(job % p.parts);
-  if (row >= p.B * p.K || p.finished[row]) return;
-  const char* base = static_cast<const char*>(p.logits) + (long long)row * p.stride * (BF ? 2 : 4);
-  const int nv = (p.V + VE - 1) / VE;
-  const int v0 = part * p.vecs, v1 = min(nv, v0 + p.vecs);
-
-  float X = kLowest, best = -INFINITY;
-  int at = v0 + lane < v1 ? v0 + lane : INT_MAX;
-  double sum = 0.0;
-  for (int v = v0 + lane; v < v1; v += 64) {
-    float x[VE];
-    Row<BF>::load(base, v * VE, p.V, -INFINITY, x);
-    float mx = x[0];
-#pragma unroll
-    for (int j = 1; j < VE; ++j) mx = fmaxf(mx, x[j]);
-    if (mx > best) {
-      best = mx;
-      at = v;
-      if (mx > X + 16.f) {
-        sum *= exp((double)X - (double)mx);
-        X = mx;
-      }
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < VE; ++j) {
-      const float d = x[j] - X;
-      s += __builtin_amdgcn_exp2f(fmaf(d, kL2eHi, d * kL2eLo));
-    }
-    sum += (double)s;
-  }
-  // the part's sum: lanes in a fixed order of pairs
-  const float Xw = wave_max(X);
-  double sw = sum * exp((double)X - (double)Xw);
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) sw += __shfl_xor(sw, o);
-  const long long out = (long long)row * p.parts + part;
-  if (lane == 0) {
-    p.part_sum[out] = sw;
-    p.part_m[out] = Xw;
-  }
-
   float last_v = INFINITY;
   int last_i = -1;
   for (int r = 0; r < p.K; ++r) {
@@ -230,10 +221,10 @@ __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
     }
     after(ev, ei, bv, bi);
     n = wave_best(bv, bi);
-    const float nv2 = lane_f(bv, n);
+    const float nv = lane_f(bv, n);
     const int ni = __builtin_amdgcn_readlane(bi, n);
     if (lane == w) {
-      best = nv2;
+      best = nv;
       at = ni == INT_MAX ? INT_MAX : ni / VE;
       last_v = ev;
       last_i = ei;
@@ -241,59 +232,211 @@ __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
   }
 }
 
+template <bool BF>
+__global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
+  constexpr int VE = Row<BF>::VE;
+  __shared__ float kept_v[4][kKept];
+  __shared__ int kept_i[4][kKept];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const long long job = (long long)blockIdx.x * 4 + wave;
+  const int row = (int)(job / p.parts), part = (int)(job % p.parts);
+  if (row >= p.B * p.K || p.finished[row]) return;
+  const char* base = static_cast<const char*>(p.logits) + (long long)row * p.stride * (BF ? 2 : 4);
+  const int nv = (p.V + VE - 1) / VE;
+  const int v0 = part * p.vecs, v1 = min(nv, v0 + p.vecs);
+
+  float X = kLowest, best = -INFINITY;
+  int at = v0 + lane < v1 ? v0 + lane : INT_MAX;
+  double sum = 0.0;
+  auto take = [&](int v, const float (&x)[VE]) {
+    float mx = x[0];
+#pragma unroll
+    for (int j = 1; j < VE; ++j) mx = fmaxf(mx, x[j]);
+    if (mx > best) {
+      best = mx;
+      at = v;
+      if (mx > X + 16.f) {
+        sum *= exp((double)X - (double)mx);
+        X = mx;
+      }
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      const float d = x[j] - X;
+      s += __builtin_amdgcn_exp2f(fmaf(d, kL2eHi, d * kL2eLo));
+    }
+    sum += (double)s;
+  };
+  int v = v0 + lane;
+  // whole vectors of the row, kAhead at a time
+  const int whole = min(v1, p.V / VE);
+  for (; v + 64 * (kAhead - 1) < whole; v += 64 * kAhead) {
+    typename Row<BF>::Raw u[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) u[a] = Row<BF>::raw(base, (v + 64 * a) * VE);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      float x[VE];
+      Row<BF>::split(u[a], x);
+      take(v + 64 * a, x);
+    }
+  }
+  for (; v < v1; v += 64) {
+    float x[VE];
+    Row<BF>::load(base, v * VE, p.V, -INFINITY, x);
+    take(v, x);
+  }
+  // the part's sum: lanes in a fixed order of pairs
+  const float Xw = wave_max(X);
+  double sw = sum * exp((double)X - (double)Xw);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) sw += __shfl_xor(sw, o);
+  const long long out = (long long)row * p.parts + part;
+  if (lane == 0) {
+    p.part_sum[out] = sw;
+    p.part_m[out] = Xw;
+  }
+
+  // the K lanes whose bests come first, the last of them the bound
+  float bound = -INFINITY, hv = best;
+  int hi = at, lanes = 0, chosen = 0;
+  for (; chosen < p.K; ++chosen) {
+    const int w = wave_best(hv, hi);
+    if (__builtin_amdgcn_readlane(hi, w) == INT_MAX) {  // fewer lanes than K have values: all of theirs count
+      bound = -INFINITY;
+      break;
+    }
+    bound = lane_f(hv, w);
+    if (lane == chosen) lanes = w;
+    if (lane == w) hv = -INFINITY, hi = INT_MAX;
+  }
+  // their values that reach it
+  const int each = (v1 - v0 + 63) / 64, total = chosen * each;
+  int kept = 0;
+  for (int t = lane; t - lane < total; t += 64) {
+    const int w = __shfl(lanes, min(t / each, chosen - 1));
+    const int u = v0 + w + 64 * (t % each);
+    const bool in = t < total && u < v1;
+    float x[VE];
+    if (in)
+      Row<BF>::load(base, u * VE, p.V, NAN, x);
+    else
+#pragma unroll
+      for (int j = 0; j < VE; ++j) x[j] = NAN;
+    float mx = x[0];
+#pragma unroll
+    for (int j = 1; j < VE; ++j) mx = fmaxf(mx, x[j]);
+    if (!__any(mx >= bound)) continue;
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      const unsigned long long who = __ballot(x[j] >= bound);
+      if (x[j] >= bound) {
+        const int pos = kept + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
+                                                         __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+        if (pos < kKept) {
+          kept_v[wave][pos] = x[j];
+          kept_i[wave][pos] = u * VE + j;
+        }
+      }
+      kept += __popcll(who);
+    }
+  }
+  if (kept > kKept) {
+    part_best_by_one<BF>(p, base, v0, v1, best, at, out);
+    return;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  float cv = -INFINITY, ov = -INFINITY;
+  int ci = INT_MAX, oi = INT_MAX;
+  if (lane < kept) {
+    cv = kept_v[wave][lane];
+    ci = kept_i[wave][lane];
+  }
+  for (int r = 0; r < p.K; ++r) {
+    const int w = wave_best(cv, ci);
+    const float ev = lane_f(cv, w);
+    const int ei = __builtin_amdgcn_readlane(ci, w);
+    if (lane == r) ov = ev, oi = ei;
+    if (lane == w) cv = -INFINITY, ci = INT_MAX;
+  }
+  if (lane < p.K) {
+    p.part_val[out * p.K + lane] = ov;
+    p.part_idx[out * p.K + lane] = oi;
+  }
+}
+
 // ---- join ---------------------------------------------------------------------
-__global__ void __launch_bounds__(256) beam_join_kernel(BeamParams p) {
+constexpr int kJoinWaves = 4;
+
+__global__ void __launch_bounds__(kJoinWaves * 64) beam_join_kernel(BeamParams p) {
+  __shared__ float heads_v[kJoinWaves][kMaxParts * kMaxK];  // a beam's parts' best
+  __shared__ int heads_i[kJoinWaves][kMaxParts * kMaxK];
   __shared__ float val[kMaxK][kMaxK];  // the beams' best, in order
   __shared__ int idx[kMaxK][kMaxK];
+  __shared__ double lses[kMaxK], pens[kMaxK];
   __shared__ int parent[kMaxK];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int b = blockIdx.x / p.copies, copy = blockIdx.x % p.copies;
   const int K = p.K;
 
-  // the K best of every beam
-  for (int k = wave; k < K; k += 4) {
+  // log-sum-exp and K best of every beam: lane i holds part i's next value
+  for (int k = wave; k < K; k += kJoinWaves) {
     const int row = b * K + k;
-    if (p.finished[row]) continue;
-    const long long at = (long long)row * p.parts + lane;
-    int j = 0;
-    float v = -INFINITY;
-    int i = INT_MAX;
+    const bool fin = p.finished[row] != 0;
+    if (lane == 0) pens[k] = pow((5.0 + (p.lengths[row] + (fin ? 0 : 1))) / 6.0, (double)p.alpha);
+    if (fin) continue;
+    const long long at = (long long)row * p.parts;
+    float M = kLowest;
+    double s = 0.0;
     if (lane < p.parts) {
-      v = p.part_val[at * K];
-      i = p.part_idx[at * K];
+      M = p.part_m[at + lane];
+      s = p.part_sum[at + lane];
+    }
+    for (int i = lane; i < p.parts * K; i += 64) {
+      heads_v[wave][i] = p.part_val[at * K + i];
+      heads_i[wave][i] = p.part_idx[at * K + i];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    const float Mw = wave_max(M);
+    s *= exp((double)M - (double)Mw);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
+    // no distribution: NaN or +inf among the logits, or all -inf
+    if (lane == 0) lses[k] = s > 0.0 && s < INFINITY ? (double)Mw + log(s) : (double)NAN;
+    int j = 0, i = INT_MAX;
+    float v = -INFINITY;
+    if (lane < p.parts) {
+      v = heads_v[wave][lane * K];
+      i = heads_i[wave][lane * K];
     }
     for (int r = 0; r < K; ++r) {
       const int w = wave_best(v, i);
       if (lane == w) {
         val[k][r] = v;
         idx[k][r] = i;
-        ++j;
-        v = j < K ? p.part_val[at * K + j] : -INFINITY;
-        i = j < K ? p.part_idx[at * K + j] : INT_MAX;
+        const bool more = lane < p.parts && ++j < K;
+        v = more ? heads_v[wave][lane * K + j] : -INFINITY;
+        i = more ? heads_i[wave][lane * K + j] : INT_MAX;
       }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
   }
   __syncthreads();
 
   // the K best of all: lane k holds beam k's next proposal
   if (wave == 0) {
     const bool beam = lane < K;
-    const int row = b * K + (beam ? lane : 0);
+    const int k = beam ? lane : 0, row = b * K + k;
     const bool fin = p.finished[row] != 0;
     const double score = p.scores[row];
     const int n = p.lengths[row] + (fin ? 0 : 1);
-    const double pen = pow((5.0 + n) / 6.0, (double)p.alpha);
-    double lse = 0.0;
-    bool none = !(score > -INFINITY) || score == INFINITY;  // proposes rank -inf only
-    if (beam && !fin) {
-      float M = kLowest;
-      const long long at = (long long)row * p.parts;
-      for (int i = 0; i < p.parts; ++i) M = fmaxf(M, p.part_m[at + i]);
-      double s = 0.0;
-      for (int i = 0; i < p.parts; ++i) s += p.part_sum[at + i] * exp((double)p.part_m[at + i] - (double)M);
-      lse = (double)M + log(s);
-      none = none || !(s > 0.0) || s == INFINITY;
-    }
+    const double pen = pens[k], lse = fin ? 0.0 : lses[k];
+    // proposes rank -inf only
+    const bool none = !(score > -INFINITY) || score == INFINITY || isnan(lse);
     int j = 0, tok = 0;
     double cand = -INFINITY, rank = -INFINITY;
     auto next = [&]() {
@@ -307,8 +450,8 @@ __global__ void __launch_bounds__(256) beam_join_kernel(BeamParams p) {
         tok = j == 0 ? p.eos : (j - 1 < p.eos ? j - 1 : j);
         cand = j == 0 ? score : -INFINITY;
       } else {
-        tok = idx[lane][j];
-        cand = score + ((double)val[lane][j] - lse);
+        tok = idx[k][j];
+        cand = score + ((double)val[k][j] - lse);
       }
       rank = cand / pen;
     };
@@ -316,16 +459,14 @@ __global__ void __launch_bounds__(256) beam_join_kernel(BeamParams p) {
     for (int r = 0; r < K; ++r) {
       // the largest rank, of equals the lowest beam (its next proposal precedes every other beam's token)
       double br = rank;
-      int bk = lane;
-      bool live = tok != INT_MAX;
-      if (!live) bk = INT_MAX;
+      int bk = tok != INT_MAX ? lane : INT_MAX;
 #pragma unroll
       for (int o = 1; o < kMaxK; o <<= 1) {
         const double orr = __shfl_xor(br, o);
         const int ok = __shfl_xor(bk, o);
-        const bool take = ok != INT_MAX && (bk == INT_MAX || orr > br || (orr == br && ok < bk));
-        br = take ? orr : br;
-        bk = take ? ok : bk;
+        const bool better = ok != INT_MAX && (bk == INT_MAX || orr > br || (orr == br && ok < bk));
+        br = better ? orr : br;
+        bk = better ? ok : bk;
       }
       if (lane == bk) {
         parent[r] = lane;
@@ -345,7 +486,7 @@ __global__ void __launch_bounds__(256) beam_join_kernel(BeamParams p) {
   __syncthreads();
 
   // the chosen beams' states
-  const int part = copy * 256 + tid, all = p.copies * 256;
+  const int part = copy * (kJoinWaves * 64) + tid, all = p.copies * (kJoinWaves * 64);
   const long long BK = (long long)p.B * K;
   for (int which = 0; which < 2; ++which) {
     const char* src = which ? p.c : p.h;

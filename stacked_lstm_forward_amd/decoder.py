@@ -25,7 +25,7 @@ import ctypes
 from dataclasses import dataclass
 from typing import Optional
 
-from . import LSTM_BF16, LSTM_F32, _ptr, _stream, check, load_library
+from . import LSTM_BF16, LSTM_F32, LSTM_OK, _ptr, _stream, check, load_library
 
 EXPORTED = ("lstm_attn_validate", "lstm_attn_workspace_size", "lstm_attn_bwd_workspace_size", "lstm_attn_fwd",
             "lstm_attn_bwd", "lstm_beam_workspace_size", "lstm_beam_step")
@@ -103,6 +103,15 @@ def lstm_beam_step(desc, logits, scores, finished, lengths, tokens, parents, sco
                                      _stream(stream)))
 
 
+def _on(stream, t) -> int:
+    """The stream's handle; by default the current stream of t's device (a single token's launch is
+    short beside building a torch.cuda.Stream object, so the handle is asked for directly)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return _stream(stream)
+
+
 # ---- checks of tensors (host only) --------------------------------------------
 
 
@@ -172,8 +181,13 @@ class AttnProblem:
 
     def forward(self, stream=None) -> None:
         """o [B, Tq, Hq, D] and lse [B, Hq, Tq]."""
-        check(lstm_attn_fwd(self.desc, self.q, self.k, self.v, self.kv_len, self.key_mask, self.o, self.lse, self.ws,
-                            stream), "lstm_attn_fwd")
+        n, m, e = self.kv_len, self.key_mask, self.lse
+        st = _lib().lstm_attn_fwd(self.desc, self.q.data_ptr(), self.k.data_ptr(), self.v.data_ptr(),
+                                  None if n is None else n.data_ptr(), None if m is None else m.data_ptr(),
+                                  self.o.data_ptr(), None if e is None else e.data_ptr(), self.ws.data_ptr(),
+                                  _on(stream, self.q))
+        if st != LSTM_OK:
+            check(st, "lstm_attn_fwd")
 
     def backward(self, dout, stream=None) -> None:
         """dq, dk, dv from dout, a tensor like o, after a forward() of the same inputs."""
@@ -182,7 +196,7 @@ class AttnProblem:
         _like(dout, "dout", self.o.shape, self.o.dtype, self.o.device, dense=False)
         self.desc.dout = _rows(dout, "dout")
         check(lstm_attn_bwd(self.desc, self.q, self.k, self.v, self.kv_len, self.key_mask, self.o, self.lse, dout,
-                            self.dq, self.dk, self.dv, self.bws, stream), "lstm_attn_bwd")
+                            self.dq, self.dk, self.dv, self.bws, _on(stream, self.q)), "lstm_attn_bwd")
 
 
 def attn_desc(q, k, v, scale: Optional[float] = None) -> AttnDesc:
@@ -261,7 +275,8 @@ class BeamProblem:
         """One selection: tokens, parents, scores_out, finished_out, lengths_out [B, K], states_out."""
         check(lstm_beam_step(self.desc, self.logits, self.scores, self.finished, self.lengths, self.tokens,
                              self.parents, self.scores_out, self.finished_out, self.lengths_out, self.states[0],
-                             self.states[1], self.states_out[0], self.states_out[1], self.ws, stream),
+                             self.states[1], self.states_out[0], self.states_out[1], self.ws,
+                             _on(stream, self.logits)),
               "lstm_beam_step")
 
     def advance(self) -> None:
