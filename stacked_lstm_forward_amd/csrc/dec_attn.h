@@ -303,6 +303,86 @@ __device__ __forceinline__ uint4 load16(const char* row, int byte, int dbytes, b
   return ok && byte < dbytes ? *reinterpret_cast<const uint4*>(row + byte) : make_uint4(0, 0, 0, 0);
 }
 
+// Zero-initialised first products: s[kt][qc] = rows of `tile` * frag columns.
+template <typename T, int DP, int QC, int KT>
+__device__ __forceinline__ void mma_rows0(f32x4 (&s)[KT / 16][QC], const char* tile,
+                                          const uint4 (&b)[QC][DP * AT<T>::SZ / 64], int lane) {
+#pragma unroll
+  for (int kt = 0; kt < KT / 16; ++kt)
+#pragma unroll
+    for (int qc = 0; qc < QC; ++qc) s[kt][qc] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  mma_rows<T, DP, QC, KT>(s, tile, b, lane);
+}
+
+// A workgroup's copy of KT rows of one tensor to LDS, in two halves: load() issues
+// the global reads a tile ahead, store() writes what arrived.  Rows at or past
+// `end` are read as row end-1: a key past the last gets the bias -inf, and a
+// copy of a valid key brings no infinity or NaN that the valid one does not.
+// Columns at or past D are written as zeros, and so are rows whose key mask byte
+// (read beside them) is 0.  Full tiles are addressed by a running pointer.
+template <typename T, int DP, int KT, int NT>
+struct TileCopy {
+  static constexpr int SZ = AT<T>::SZ, PB = Pitch<T, DP>::B, VR = DP * SZ / 16;
+  static constexpr int NV = (KT * VR + NT - 1) / NT;
+  static constexpr bool EVEN = KT * VR % NT == 0;
+  const char* at[NV];  // this thread's pieces of the tile at key `s`
+  uint4 x[NV];
+  uint8_t m[NV];
+  const char* base;
+  long long step;
+
+  __device__ __forceinline__ void init(const char* b, long long st, int s, int tid, int db) {
+    base = b;
+    step = st;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = tid + j * NT, c = (i % VR) * 16;
+      at[j] = b + (s + (EVEN || i < KT * VR ? i / VR : 0)) * st + (c < db ? c : 0);
+    }
+  }
+  // loads the tile at s, which is the one init() named or the one after the last loaded
+  __device__ __forceinline__ void load(int s, int end, const uint8_t* mb, int tid, int db) {
+    if (s + KT <= end) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        x[j] = *reinterpret_cast<const uint4*>(at[j]);
+        at[j] += KT * step;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int i = tid + j * NT, c = (i % VR) * 16;
+        const int r = min(s + (EVEN || i < KT * VR ? i / VR : 0), end - 1);
+        x[j] = *reinterpret_cast<const uint4*>(base + r * step + (c < db ? c : 0));
+      }
+    }
+    if (mb) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int i = tid + j * NT;
+        m[j] = mb[min(s + (EVEN || i < KT * VR ? i / VR : 0), end - 1)];
+      }
+    }
+  }
+  __device__ __forceinline__ void store(char* to, const uint8_t* mb, int tid, int db) {
+    if (mb) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (!m[j]) x[j] = make_uint4(0, 0, 0, 0);
+    }
+    if (db < DP * SZ) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (((tid + j * NT) % VR) * 16 >= db) x[j] = make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = tid + j * NT, a = (i / VR) * PB + (i % VR) * 16;
+      if (EVEN || i < KT * VR) *reinterpret_cast<uint4*>(to + a) = x[j];
+    }
+  }
+};
+
 // Number of keys of sentence b before the key mask.
 __device__ __forceinline__ int keys_of(const AttnParams& p, int b) {
   int n = p.S;

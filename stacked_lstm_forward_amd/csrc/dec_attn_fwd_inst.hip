@@ -13,10 +13,9 @@ typedef float ET;
 #endif
 constexpr int DP = DEC_DP;
 
-// The scores x of a tile become exponentials; m, l and o follow.
-template <typename T, int DP, int QC, int KT, int NTILES>
-__device__ __forceinline__ void softmax_tile(f32x4 (&x)[KT / 16][QC], f32x4 (&o)[NTILES][QC], float (&m)[QC],
-                                             float (&l)[QC], float scale_log2) {
+// The maximum of a tile's scores (base-2 units), one per column.
+template <int QC, int KT>
+__device__ __forceinline__ void tile_max(const f32x4 (&x)[KT / 16][QC], float (&mn)[QC], float scale_log2) {
 #pragma unroll
   for (int qc = 0; qc < QC; ++qc) {
     float mx = x[0][qc][0];
@@ -24,29 +23,53 @@ __device__ __forceinline__ void softmax_tile(f32x4 (&x)[KT / 16][QC], f32x4 (&o)
     for (int kt = 0; kt < KT / 16; ++kt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) mx = fmaxf(mx, x[kt][qc][i]);
-    // The maximum in use stays until it is 2^8 behind: exponentials up to 2^8
-    // are as exact as those below 1, and o is rescaled for few tiles only.
-    const float mn = col_max(mx) * scale_log2;
-    if (__any(mn > m[qc] + 8.f)) {
-      const float mu = fmaxf(m[qc], mn);
+    mn[qc] = col_max(mx) * scale_log2;
+  }
+}
+
+// The maximum in use stays until it is 2^8 behind: exponentials up to 2^8 are as
+// exact as those below 1, and o is rescaled for few tiles only.
+template <int QC, int NTILES>
+__device__ __forceinline__ void raise_max(const float (&mn)[QC], f32x4 (&o)[NTILES][QC], float (&m)[QC],
+                                          float (&l)[QC]) {
+#pragma unroll
+  for (int qc = 0; qc < QC; ++qc) {
+    if (__any(mn[qc] > m[qc] + 8.f)) {
+      const float mu = fmaxf(m[qc], mn[qc]);
       const float alpha = mu == -INFINITY ? 1.f : exp2_fast(m[qc] - mu);
       m[qc] = mu;
       l[qc] *= alpha;
 #pragma unroll
       for (int n = 0; n < NTILES; ++n) o[n][qc] *= alpha;
     }
-    const float mu = m[qc] == -INFINITY ? 0.f : m[qc];
-    float sum = 0.f;
+  }
+}
+
+// Scores become exponentials, their sum goes to l.
+template <int QC, int KT>
+__device__ __forceinline__ void tile_exp(f32x4 (&x)[KT / 16][QC], const float (&m)[QC], float (&l)[QC],
+                                         float scale_log2) {
 #pragma unroll
-    for (int kt = 0; kt < KT / 16; ++kt)
+  for (int kt = 0; kt < KT / 16; ++kt)
+#pragma unroll
+    for (int qc = 0; qc < QC; ++qc) {
+      const float mu = m[qc] == -INFINITY ? 0.f : m[qc];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float e = exp2_fast(fmaf(x[kt][qc][i], scale_log2, -mu));
         x[kt][qc][i] = e;
-        sum += e;
+        l[qc] += e;
       }
-    l[qc] += sum;
-  }
+    }
+}
+
+template <typename T, int DP, int QC, int KT, int NTILES>
+__device__ __forceinline__ void softmax_tile(f32x4 (&x)[KT / 16][QC], f32x4 (&o)[NTILES][QC], float (&m)[QC],
+                                             float (&l)[QC], float scale_log2) {
+  float mn[QC];
+  tile_max<QC, KT>(x, mn, scale_log2);
+  raise_max<QC, NTILES>(mn, o, m, l);
+  tile_exp<QC, KT>(x, m, l, scale_log2);
 }
 
 // One column group's results, to o and lse or to the parts of a split.
@@ -76,8 +99,7 @@ __device__ __forceinline__ void store_rows(const AttnParams& p, int b, int hk, i
 template <typename T, int DP, int QC, int NW, int KT>
 __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
   constexpr int SZ = AT<T>::SZ, NT = NW * 64, PB = Pitch<T, DP>::B;
-  constexpr int NCH = DP * SZ / 64, VR = DP * SZ / 16;  // 16-byte pieces of a row
-  constexpr int NV = (KT * VR + NT - 1) / NT;           // pieces per thread and tile
+  constexpr int NCH = DP * SZ / 64;  // 64-byte chunks of a row
   constexpr int NTILES = DP / 16;
   // two buffers: a tile is written while its predecessor is read, one barrier a tile
   __shared__ __align__(16) char skb[2][KT * PB];
@@ -120,55 +142,65 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
     for (int n = 0; n < NTILES; ++n) o[n][qc] = (f32x4){0.f, 0.f, 0.f, 0.f};
   }
 
-  // A tile's loads are issued a tile ahead; key mask bytes come with them and are applied on the way to LDS.
-  uint4 rk[NV], rv[NV];
-  uint8_t rm[NV], rb = 0;
-  auto load = [&](int s) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = tid + j * NT, r = s + i / VR, c = (i % VR) * 16;
-      const bool ok = (KT * VR % NT == 0 || i < KT * VR) && r < s1;
-      if (mb) rm[j] = ok ? mb[r] : 0;
-      rk[j] = load16(kb + r * p.sk.t, c, db, ok);
-      rv[j] = load16(vb + r * p.sv.t, c, db, ok);
-    }
+  TileCopy<T, DP, KT, NT> ck, cv;
+  uint8_t rb = 0;
+  auto load_k = [&](int s) {
+    ck.load(s, s1, mb, tid, db);
     if (tid < KT) rb = s + tid < s1 ? (mb ? mb[s + tid] : 1) : 0;
   };
-  auto store = [&](int buf) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = tid + j * NT, a = (i / VR) * PB + (i % VR) * 16;
-      if (KT * VR % NT == 0 || i < KT * VR) {
-        if (mb && !rm[j]) rk[j] = rv[j] = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(skb[buf] + a) = rk[j];
-        *reinterpret_cast<uint4*>(svb[buf] + a) = rv[j];
-      }
-    }
+  auto store_k = [&](int buf) {
+    ck.store(skb[buf], mb, tid, db);
     if (tid < KT) sbiasb[buf][tid] = rb ? 0.f : -INFINITY;
   };
+  // -inf where a tile has keys left out
+  auto leave_out = [&](f32x4 (&x)[KT / 16][QC], int s, int buf) {
+    if (mb || s + KT > s1) {
+#pragma unroll
+      for (int kt = 0; kt < KT / 16; ++kt) {
+        const f32x4 bias = *reinterpret_cast<const f32x4*>(sbiasb[buf] + kt * 16 + (lane >> 4) * 4);
+#pragma unroll
+        for (int qc = 0; qc < QC; ++qc) x[kt][qc] += bias;
+      }
+    }
+  };
+
+  // Tile i's exponentials are taken beside the matrix products of tile i+1's scores.
+  // k is a tile ahead of v in LDS; a buffer is written one barrier after its last read.
+  f32x4 xa[KT / 16][QC], xb[KT / 16][QC];
+  float mn[QC];
   if (s0 < s1) {
-    load(s0);
-    store(0);
+    ck.init(kb, p.sk.t, s0, tid, db);
+    cv.init(vb, p.sv.t, s0, tid, db);
+    load_k(s0);
+    cv.load(s0, s1, mb, tid, db);
+    store_k(0);
+    if (s0 + KT < s1) load_k(s0 + KT);
+    cv.store(svb[0], mb, tid, db);
+    if (s0 + KT < s1) store_k(1);
+    __syncthreads();
+    mma_rows0<T, DP, QC, KT>(xa, skb[0], qf, lane);
+    leave_out(xa, s0, 0);
+    tile_max<QC, KT>(xa, mn, p.scale_log2);
     __syncthreads();
   }
-  int buf = 0;
-  for (int s = s0; s < s1; s += KT, buf ^= 1) {
-    const char *sk = skb[buf], *sv = svb[buf];
-    const float* sbias = sbiasb[buf];
-    if (s + KT < s1) load(s + KT);
-
-    f32x4 x[KT / 16][QC];
-#pragma unroll
-    for (int kt = 0; kt < KT / 16; ++kt) {
-      const f32x4 bias = *reinterpret_cast<const f32x4*>(sbias + kt * 16 + (lane >> 4) * 4);
-#pragma unroll
-      for (int qc = 0; qc < QC; ++qc) x[kt][qc] = bias;
-    }
-    mma_rows<T, DP, QC, KT>(x, sk, qf, lane);
-    softmax_tile<T, DP, QC, KT, NTILES>(x, o, m, l, p.scale_log2);
-    mma_tr<T, DP, QC, KT, NTILES>(o, sv, x, lane);
-    if (s + KT < s1) store(buf ^ 1);
+  auto step = [&](f32x4 (&x)[KT / 16][QC], f32x4 (&y)[KT / 16][QC], int s, int buf) {
+    const bool more = s + KT < s1, more2 = s + 2 * KT < s1;
+    if (more2) load_k(s + 2 * KT);
+    if (more) cv.load(s + KT, s1, mb, tid, db);
+    raise_max<QC, NTILES>(mn, o, m, l);
+    mma_rows0<T, DP, QC, KT>(y, skb[buf ^ 1], qf, lane);  // of stale rows after the last tile: not used
+    tile_exp<QC, KT>(x, m, l, p.scale_log2);
+    mma_tr<T, DP, QC, KT, NTILES>(o, svb[buf], x, lane);
+    leave_out(y, s + KT, buf ^ 1);
+    tile_max<QC, KT>(y, mn, p.scale_log2);
+    if (more2) store_k(buf);
+    if (more) cv.store(svb[buf ^ 1], mb, tid, db);
     __syncthreads();
+  };
+  for (int s = s0; s < s1; s += 2 * KT) {
+    step(xa, xb, s, 0);
+    if (s + KT >= s1) break;
+    step(xb, xa, s + KT, 1);
   }
 
 #pragma unroll

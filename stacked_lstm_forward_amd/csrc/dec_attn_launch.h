@@ -30,7 +30,7 @@ hipError_t attn_delta_launch(const AttnParams&, bool bf16, hipStream_t);
 constexpr int fwd_columns(bool bf16) { return bf16 ? 2 : 1; }
 constexpr int fwd_key_tile(bool bf16, int dp) { return bf16 && dp <= 160 ? 64 : 32; }
 // eight waves share a tile where their operands and sums fit 256 registers a lane
-constexpr int fwd_max_waves(bool bf16, int dp) { return bf16 && dp > 160 ? 4 : 8; }
+constexpr int fwd_max_waves(bool bf16, int dp) { return bf16 && dp > 128 ? 4 : 8; }
 constexpr int fwd_waves(bool bf16, int dp, int rows) {
   return rows <= 32 ? 0 : rows <= 64 * fwd_columns(bf16) ? 4 : fwd_max_waves(bf16, dp);
 }
