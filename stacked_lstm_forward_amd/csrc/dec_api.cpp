@@ -120,7 +120,7 @@ size_t lstm_attn_workspace_size(const lstm_attn_desc_t* d) {
 
 size_t lstm_attn_bwd_workspace_size(const lstm_attn_desc_t* d) {
   if (check_desc(d, true) != LSTM_OK) return 0;
-  return round256((size_t)d->B * d->Hq * d->Tq * sizeof(float));
+  return round256((size_t)d->B * d->Hq * d->Tq * 2 * sizeof(float));
 }
 
 lstm_status_t lstm_attn_fwd(const lstm_attn_desc_t* d, const void* q, const void* k, const void* v,
@@ -158,12 +158,9 @@ lstm_status_t lstm_attn_bwd(const lstm_attn_desc_t* d, const void* q, const void
   p.q = (const char*)q, p.k = (const char*)k, p.v = (const char*)v, p.o_in = (const char*)o, p.lse_in = lse;
   p.dout = (const char*)dout, p.dq = (char*)dq, p.dk = (char*)dk, p.dv = (char*)dv;
   p.kv_len = kv_len, p.key_mask = key_mask;
-  p.delta = (float*)ws;
+  p.stats = (float*)ws;
   const bool bf = d->dtype == LSTM_BF16;
-  const int per = 64 * bwd_columns(bf, (dp_index(d->D) + 1) * 32);
-  p.tiles = (p.rows + per - 1) / per;
-  p.kv_tiles = (p.S + per - 1) / per;
-  if (attn_delta_launch(p, bf, stream) != hipSuccess) return LSTM_ERR_HIP;
+  if (attn_stats_launch(p, bf, stream) != hipSuccess) return LSTM_ERR_HIP;
   if (kBwd[bf][dp_index(d->D)](p, stream) != hipSuccess) return LSTM_ERR_HIP;
   return LSTM_OK;
 }

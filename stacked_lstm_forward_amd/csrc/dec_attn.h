@@ -48,8 +48,10 @@ struct AttnParams {
   float scale, scale_log2;  // scale, scale * log2(e)
   float* part_o;         // nsplit > 1: [B*Hkv*rows][nsplit][D] unnormalised
   float* part_ml;        // [B*Hkv*rows][nsplit][2]: maximum (base-2 units) and sum
-  float* delta;          // backward: [B][Hq][Tq]
-  int blocks_a;          // backward: blocks of the key-side part
+  float* stats;          // backward: [B*Hkv][rows][2], -lse (base-2 units) and -delta
+  int blocks_a;          // backward: workgroups that own keys
+  int row_dg;            // backward: a tile of rows ahead, heads of the group and bytes of q and dout
+  long long row_q0, row_q1, row_d0, row_d1;  // (.1: where the head passes the group's end)
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -314,12 +316,35 @@ __device__ __forceinline__ void mma_rows0(f32x4 (&s)[KT / 16][QC], const char* t
   mma_rows<T, DP, QC, KT>(s, tile, b, lane);
 }
 
+// The same with the columns' operands in LDS.
+template <typename T, int DP, int QC, int KT>
+__device__ __forceinline__ void mma_rows0_lds(f32x4 (&s)[KT / 16][QC], const char* tile,
+                                              const uint4 (*b)[QC][64], int lane) {
+  constexpr int PB = Pitch<T, DP>::B;
+  const char* base = tile + (lane & 15) * PB + (lane >> 4) * 16;
+#pragma unroll
+  for (int kt = 0; kt < KT / 16; ++kt)
+#pragma unroll
+    for (int qc = 0; qc < QC; ++qc) s[kt][qc] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < DP * AT<T>::SZ / 64; ++c) {
+    uint4 f[QC];
+#pragma unroll
+    for (int qc = 0; qc < QC; ++qc) f[qc] = b[c][qc][lane];
+#pragma unroll
+    for (int kt = 0; kt < KT / 16; ++kt) {
+      const uint4 a = *reinterpret_cast<const uint4*>(base + kt * 16 * PB + c * 64);
+#pragma unroll
+      for (int qc = 0; qc < QC; ++qc) mma_chunk<T>(s[kt][qc], a, f[qc]);
+    }
+  }
+}
+
 // A workgroup's copy of KT rows of one tensor to LDS, in two halves: load() issues
 // the global reads a tile ahead, store() writes what arrived.  Rows at or past
-// `end` are read as row end-1: a key past the last gets the bias -inf, and a
-// copy of a valid key brings no infinity or NaN that the valid one does not.
-// Columns at or past D are written as zeros, and so are rows whose key mask byte
-// (read beside them) is 0.  Full tiles are addressed by a running pointer.
+// `end` (read as row end-1), columns at or past D and rows whose key mask byte
+// (read beside them) is 0 are written as zeros.  Full tiles are addressed by a
+// running pointer.
 template <typename T, int DP, int KT, int NT>
 struct TileCopy {
   static constexpr int SZ = AT<T>::SZ, PB = Pitch<T, DP>::B, VR = DP * SZ / 16;
@@ -364,7 +389,12 @@ struct TileCopy {
       }
     }
   }
-  __device__ __forceinline__ void store(char* to, const uint8_t* mb, int tid, int db) {
+  __device__ __forceinline__ void store(char* to, int s, int end, const uint8_t* mb, int tid, int db) {
+    if (s + KT > end) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (s + (tid + j * NT) / VR >= end) x[j] = make_uint4(0, 0, 0, 0);
+    }
     if (mb) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
@@ -391,7 +421,9 @@ __device__ __forceinline__ int keys_of(const AttnParams& p, int b) {
 }
 
 // Block number -> work item such that the items of one XCD (blocks go round
-// robin over the 8 XCDs) are neighbours and share their k and v in its L2.
+// robin over the 8 XCDs) are neighbours and share their k and v in its L2.  The
+// sentences follow each other within a head, so that every XCD gets short and
+// long ones.
 __device__ __forceinline__ int xcd_item(int block, int n) {
   const int per = n >> 3, extra = n & 7, x = block & 7, slot = block >> 3;
   return x * per + min(x, extra) + slot;

@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int item = xcd_item(blockIdx.x, gridDim.x);
   const int tile = item % p.tiles, rest = item / p.tiles;
-  const int split = rest % p.nsplit, bh = rest / p.nsplit;
-  const int b = bh / p.Hkv, hk = bh % p.Hkv;
+  const int split = rest % p.nsplit, pair = rest / p.nsplit;
+  const int b = pair % p.B, hk = pair / p.B, bh = b * p.Hkv + hk;
   const int db = p.D * SZ;
 
   const int s0 = split * p.kv_per_split;
@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
     ck.load(s, s1, mb, tid, db);
     if (tid < KT) rb = s + tid < s1 ? (mb ? mb[s + tid] : 1) : 0;
   };
-  auto store_k = [&](int buf) {
-    ck.store(skb[buf], mb, tid, db);
+  auto store_k = [&](int buf, int s) {
+    ck.store(skb[buf], s, s1, mb, tid, db);
     if (tid < KT) sbiasb[buf][tid] = rb ? 0.f : -INFINITY;
   };
   // -inf where a tile has keys left out
@@ -173,10 +173,10 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
     cv.init(vb, p.sv.t, s0, tid, db);
     load_k(s0);
     cv.load(s0, s1, mb, tid, db);
-    store_k(0);
+    store_k(0, s0);
     if (s0 + KT < s1) load_k(s0 + KT);
-    cv.store(svb[0], mb, tid, db);
-    if (s0 + KT < s1) store_k(1);
+    cv.store(svb[0], s0, s1, mb, tid, db);
+    if (s0 + KT < s1) store_k(1, s0 + KT);
     __syncthreads();
     mma_rows0<T, DP, QC, KT>(xa, skb[0], qf, lane);
     leave_out(xa, s0, 0);
@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
     mma_tr<T, DP, QC, KT, NTILES>(o, svb[buf], x, lane);
     leave_out(y, s + KT, buf ^ 1);
     tile_max<QC, KT>(y, mn, p.scale_log2);
-    if (more2) store_k(buf);
-    if (more) cv.store(svb[buf ^ 1], mb, tid, db);
+    if (more2) store_k(buf, s + 2 * KT);
+    if (more) cv.store(svb[buf ^ 1], s + KT, s1, mb, tid, db);
     __syncthreads();
   };
   for (int s = s0; s < s1; s += 2 * KT) {
@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l15 = lane & 15;
   const int item = xcd_item(blockIdx.x, gridDim.x);
   const int tile = item % p.tiles, rest = item / p.tiles;
-  const int split = rest % p.nsplit, bh = rest / p.nsplit;
-  const int b = bh / p.Hkv, hk = bh % p.Hkv;
+  const int split = rest % p.nsplit, pair = rest / p.nsplit;
+  const int b = pair % p.B, hk = pair / p.B, bh = b * p.Hkv + hk;
   const int db = p.D * SZ;
   const int s0 = split * p.kv_per_split;
   const int s1 = min(keys_of(p, b), s0 + p.kv_per_split);

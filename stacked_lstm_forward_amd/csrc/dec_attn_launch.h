@@ -22,7 +22,7 @@ DEC_ATTN_DECLARE(256)
 #undef DEC_ATTN_DECLARE
 
 hipError_t attn_combine_launch(const AttnParams&, bool bf16, hipStream_t);
-hipError_t attn_delta_launch(const AttnParams&, bool bf16, hipStream_t);
+hipError_t attn_stats_launch(const AttnParams&, bool bf16, hipStream_t);
 
 // The forward kernels' tile shapes, by rule on type, head size and rows.
 // Waves of a workgroup with rows of their own: 0 selects the kernel whose waves
@@ -46,5 +46,16 @@ constexpr int fwd_keys_per_block(bool bf16, int dp, int rows) {
 }
 // 16-column groups of a backward wave: two where operands and sums of that many fit the registers
 constexpr int bwd_columns(bool bf16, int dp) { return bf16 && dp <= 128 ? 2 : 1; }
+// registers that these take on the key side
+constexpr int bwd_registers(bool bf16, int dp) { return bwd_columns(bf16, dp) * dp * (bf16 ? 12 : 16) / 16; }
+// bf16 keeps two waves a SIMD: where a wave's registers are short (192 of 256
+// here), v's operands lie in LDS, in workgroups of eight waves; elsewhere four
+// waves, whose barriers hold up fewer (D 80, 32 x 200 rows over 777 keys: 78 us, 86
+// with eight).
+constexpr bool bwd_short(bool bf16, int dp) { return bf16 && bwd_registers(bf16, dp) >= 192; }
+constexpr int bwd_waves(bool bf16, int dp) { return bwd_short(bf16, dp) ? 8 : 4; }
+constexpr int bwd_waves_per_simd(bool bf16, int dp) { return bf16 || bwd_registers(bf16, dp) < 192 ? 2 : 1; }
+constexpr int bwd_row_tile(bool bf16, int dp) { return bf16 && dp <= 64 ? 64 : 32; }
+constexpr int bwd_key_tile(bool bf16, int dp) { return bf16 && dp <= 160 ? 64 : 32; }
 
 }  // namespace lstm

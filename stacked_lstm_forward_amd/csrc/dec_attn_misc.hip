@@ -1,5 +1,5 @@
 // Attention over encoder outputs: joining the parts of a split key axis, and
-// delta = <dout, o> of the backward pass.
+// the row statistics of the backward pass.
 #include "dec_attn.h"
 #include "dec_attn_launch.h"
 
@@ -56,15 +56,16 @@ hipError_t combine(const AttnParams& p, hipStream_t s) {
   return go(attn_combine_kernel<T, 64>, 64);
 }
 
-// 16 lanes a row; rows in the order of lse.
+// Row statistics of the backward pass, in the order of the row list: -lse in
+// base-2 units (-inf where the row has no key) and -delta = -<dout, o>.  16 lanes
+// a row.
 template <typename T>
-__global__ void __launch_bounds__(256) attn_delta_kernel(AttnParams p) {
+__global__ void __launch_bounds__(256) attn_stats_kernel(AttnParams p) {
   constexpr int SZ = AT<T>::SZ;
   const long long row = (long long)blockIdx.x * 16 + threadIdx.x / 16;
-  if (row >= (long long)p.B * p.Hq * p.Tq) return;
-  const int t = (int)(row % p.Tq);
-  const long long bh = row / p.Tq;
-  const int b = (int)(bh / p.Hq), h = (int)(bh % p.Hq);
+  if (row >= (long long)p.B * p.Hkv * p.rows) return;
+  const int r = (int)(row % p.rows), bh = (int)(row / p.rows);
+  const int b = bh / p.Hkv, t = r / p.G, h = (bh % p.Hkv) * p.G + r % p.G;
   const char* o = p.o_in + b * p.so.b + t * p.so.t + h * p.so.h;
   const char* d = p.dout + b * p.sdo.b + t * p.sdo.t + h * p.sdo.h;
   float sum = 0.f;
@@ -83,7 +84,10 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(AttnParams p) {
   }
 #pragma unroll
   for (int o2 = 8; o2 > 0; o2 >>= 1) sum += __shfl_xor(sum, o2);
-  if ((threadIdx.x & 15) == 0) p.delta[row] = sum;
+  if ((threadIdx.x & 15) == 0) {
+    const float ls = p.lse_in[((long long)b * p.Hq + h) * p.Tq + t];
+    reinterpret_cast<f32x2*>(p.stats)[row] = (f32x2){ls == -INFINITY ? ls : -ls * kLog2e, -sum};
+  }
 }
 
 }  // namespace
@@ -92,12 +96,12 @@ hipError_t attn_combine_launch(const AttnParams& p, bool bf16, hipStream_t s) {
   return bf16 ? combine<uint16_t>(p, s) : combine<float>(p, s);
 }
 
-hipError_t attn_delta_launch(const AttnParams& p, bool bf16, hipStream_t s) {
+hipError_t attn_stats_launch(const AttnParams& p, bool bf16, hipStream_t s) {
   const long long n = ((long long)p.B * p.Hq * p.Tq + 15) / 16;
   if (bf16)
-    hipLaunchKernelGGL((attn_delta_kernel<uint16_t>), dim3((unsigned)n), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((attn_stats_kernel<uint16_t>), dim3((unsigned)n), dim3(256), 0, s, p);
   else
-    hipLaunchKernelGGL((attn_delta_kernel<float>), dim3((unsigned)n), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((attn_stats_kernel<float>), dim3((unsigned)n), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
