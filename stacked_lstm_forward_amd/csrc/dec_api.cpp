@@ -71,17 +71,17 @@ AttnParams params(const lstm_attn_desc_t* d) {
   return p;
 }
 
-// Splits the key axis where the row tiles alone leave compute units idle: up to
-// two workgroups a compute unit, none with less than four key tiles (two of the
-// tiles that the waves of a few-rows workgroup take together).
+// Splits the key axis where the row tiles alone leave compute units idle: one
+// workgroup a compute unit, none with less than four key tiles (two of the tiles
+// that the waves of a few-rows workgroup take together).
 void plan_fwd(const lstm_attn_desc_t* d, AttnParams* p) {
   const bool bf = d->dtype == LSTM_BF16;
   const int dp = (d->D + 31) / 32 * 32;
-  const int per = fwd_rows_per_block(bf, dp, p->rows), kt = fwd_keys_per_block(bf, dp, p->rows);
+  const int per = fwd_rows_per_block(bf, dp, p->rows), kt = fwd_keys_per_block(bf, dp, p->rows, p->S);
   p->tiles = (p->rows + per - 1) / per;
   const long long blocks = (long long)p->B * p->Hkv * p->tiles;
   const int ktiles = (p->S + kt - 1) / kt;
-  long long n = (2 * kComputeUnits + blocks - 1) / blocks;
+  long long n = (kComputeUnits + blocks - 1) / blocks;
   const int least = p->rows <= 32 ? 2 : 4;
   if (n > ktiles / least) n = ktiles / least;
   if (n < 1) n = 1;

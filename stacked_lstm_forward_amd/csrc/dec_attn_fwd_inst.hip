@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
   constexpr int NV = KT * VR / 64;
   static_assert(KT * VR % 64 == 0, "tile divides over the wave");
   constexpr int NTILES = DP / 16;
-  constexpr int kTiles = NW * KT * PB, kJoin = QC * 16 * (DP + 4) * 4;
+  constexpr int kTiles = NW * KT * PB, kJoin = NW * QC * 16 * (DP + 4) * 4;
   __shared__ __align__(16) char smem[kTiles > kJoin ? kTiles : kJoin];
   __shared__ float sm[NW][QC * 16], sl[NW][QC * 16];
 
@@ -321,7 +321,10 @@ __global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
     __builtin_amdgcn_wave_barrier();
   }
 
-  // join the waves: common maximum, then the sums in wave order
+  // join the waves: their sums side by side in LDS, then 4 columns of a row a
+  // thread, in wave order
+  float* so = reinterpret_cast<float*>(smem);
+  if (NW > 1) __syncthreads();
 #pragma unroll
   for (int qc = 0; qc < QC; ++qc) {
     l[qc] = col_sum(l[qc]);
@@ -329,44 +332,39 @@ __global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
       sm[wave][qc * 16 + lane] = m[qc];
       sl[wave][qc * 16 + lane] = l[qc];
     }
+    store_cols_f32<T, DP, NTILES, QC>(so + ((wave * QC + qc) * 16 + l15) * (DP + 4), o, qc, DP, lane);
   }
-  float* so = reinterpret_cast<float*>(smem);
   __syncthreads();
-  float lt[QC];
-#pragma unroll
-  for (int qc = 0; qc < QC; ++qc) {
-    const int r = qc * 16 + l15;
+  constexpr int per = DP / 4;
+  for (int i = tid; i < QC * 16 * per; i += NW * 64) {
+    const int r = i / per, d = i % per * 4, row = row0 + r;
+    if (row >= p.rows || d >= p.D) continue;
     float mt = sm[0][r];
 #pragma unroll
     for (int w = 1; w < NW; ++w) mt = fmaxf(mt, sm[w][r]);
     const float mu = mt == -INFINITY ? 0.f : mt;
-    lt[qc] = 0.f;
+    float lt = 0.f;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < NW; ++w) lt[qc] += exp2_fast(sm[w][r] - mu) * sl[w][r];
-    const float by = exp2_fast(m[qc] - mu);
-    m[qc] = mt;
-#pragma unroll
-    for (int n = 0; n < NTILES; ++n) o[n][qc] *= by;
-  }
-  for (int w = NW - 1; w > 0; --w) {
-    if (wave == w) {
-#pragma unroll
-      for (int qc = 0; qc < QC; ++qc)
-#pragma unroll
-        for (int n = 0; n < NTILES; ++n) {
-          f32x4* at = reinterpret_cast<f32x4*>(so + (qc * 16 + l15) * (DP + 4) + n * 16 + g * 4);
-          *at = w == NW - 1 ? o[n][qc] : *at + o[n][qc];
-        }
+    for (int w = 0; w < NW; ++w) {
+      const float by = exp2_fast(sm[w][r] - mu);
+      lt += by * sl[w][r];
+      x += *reinterpret_cast<const f32x4*>(so + (w * QC * 16 + r) * (DP + 4) + d) * by;
     }
-    __syncthreads();
-  }
-  if (wave != 0) return;
-#pragma unroll
-  for (int qc = 0; qc < QC; ++qc) {
-#pragma unroll
-    for (int n = 0; n < NTILES; ++n)
-      if (NW > 1) o[n][qc] += *reinterpret_cast<f32x4*>(so + (qc * 16 + l15) * (DP + 4) + n * 16 + g * 4);
-    store_rows<T, DP, QC, NTILES>(p, b, hk, bh, split, row0, qc, o, m[qc], lt[qc], lane);
+    if (p.nsplit > 1) {
+      const long long at = ((long long)bh * p.rows + row) * p.nsplit + split;
+      *reinterpret_cast<f32x4*>(p.part_o + at * p.D + d) = x;
+      if (d == 0) p.part_ml[at * 2] = mt, p.part_ml[at * 2 + 1] = lt;
+    } else {
+      const int t = row / p.G, hq = hk * p.G + row % p.G;
+      x *= lt == 0.f ? 0.f : 1.f / lt;
+      char* to = p.o + b * p.so.b + t * p.so.t + hq * p.so.h + d * SZ;
+      if constexpr (AT<T>::BF)
+        *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+      else
+        *reinterpret_cast<f32x4*>(to) = x;
+      if (d == 0 && p.lse) p.lse[((long long)b * p.Hq + hq) * p.Tq + t] = mu * kLn2 + logf(lt);
+    }
   }
 }
 
@@ -394,8 +392,9 @@ hipError_t DEC_FN(DEC_BF16, DEC_DP)(const AttnParams& p, hipStream_t s) {
   switch (fwd_waves(BF, DP, p.rows)) {
     case 0:
       if constexpr (step_max_columns(BF, DP) == 2)
-        if (step_columns(BF, DP, p.rows) == 2) return launch_step<2, 4, BF ? 32 : 16>(p, s);
-      return launch_step<1, 4, BF ? 32 : 16>(p, s);
+        if (step_columns(BF, DP, p.rows) == 2) return launch_step<2, 4, step_key_tile(BF)>(p, s);
+      if (step_waves(BF, DP, p.rows, p.S) == 8) return launch_step<1, 8, step_key_tile(BF)>(p, s);
+      return launch_step<1, 4, step_key_tile(BF)>(p, s);
     case 4: return launch<QC, 4, KT>(p, s);
     default:
       if constexpr (fwd_max_waves(BF, DP) == 8) return launch<QC, 8, KT>(p, s);

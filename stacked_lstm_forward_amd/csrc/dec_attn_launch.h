@@ -40,9 +40,14 @@ constexpr int step_columns(bool bf16, int dp, int rows) { return rows <= 16 ? 1 
 constexpr int fwd_rows_per_block(bool bf16, int dp, int rows) {
   return rows <= 32 ? 16 * step_columns(bf16, dp, rows) : fwd_waves(bf16, dp, rows) * 16 * fwd_columns(bf16);
 }
-// keys below which a workgroup of a split is not worth its launch
-constexpr int fwd_keys_per_block(bool bf16, int dp, int rows) {
-  return rows <= 32 ? (bf16 ? 128 : 64) : fwd_key_tile(bf16, dp);
+// waves of the few-rows kernel: eight where four would not take all keys at once
+constexpr int step_key_tile(bool bf16) { return bf16 ? 32 : 16; }
+constexpr int step_waves(bool bf16, int dp, int rows, int S) {
+  return step_columns(bf16, dp, rows) == 1 && S > 4 * step_key_tile(bf16) ? 8 : 4;
+}
+// keys that a workgroup takes together
+constexpr int fwd_keys_per_block(bool bf16, int dp, int rows, int S) {
+  return rows <= 32 ? step_waves(bf16, dp, rows, S) * step_key_tile(bf16) : fwd_key_tile(bf16, dp);
 }
 // 16-column groups of a backward wave: two where operands and sums of that many fit the registers
 constexpr int bwd_columns(bool bf16, int dp) { return bf16 && dp <= 128 ? 2 : 1; }
