@@ -59,7 +59,8 @@
  * finished(_out) [B][K] bytes; lengths(_out), tokens, parents [B][K] int32;
  * h [L][B*K][H] dtype, c [L][B*K][H] fp32 (each may be NULL, with its output).
  * Outputs must not overlap inputs.
- * Limits: K 1 ... 16, K <= V <= 2^20, B*K < 2^24, L*H < 2^23.
+ * Limits: K 1 ... 16, K <= V <= 2^20, B*K < 2^24, L*H < 2^23,
+ * L*B*K < 2^31.
  *
  * ---- all ------------------------------------------------------------------
  * Ownership, streams and errors as in lstm_fwd.h: every tensor pointer is a

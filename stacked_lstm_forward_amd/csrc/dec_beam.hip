@@ -1,16 +1,17 @@
-// One step of beam search (include/decoder/lstm_dec.h): two launches.
+// One step of beam search (include/decoder/lstm_dec.h): two or three launches.
 //
-//   rows   one wave per part of a beam's row of logits: reads it once, keeps the
-//          part's sum of exponentials and, per lane, the best value seen with the
-//          first 16-byte vector that holds it; then takes the part's K best in
-//          the order (value falling, index rising).  These lie in the K lanes
-//          whose best come first in that order, and none is below the last of
-//          the K lanes' bests: the wave rereads these lanes' vectors only and
-//          keeps what reaches that value.
-//   join   one sentence per workgroup (several where the states are large, each
-//          joining again): a wave per beam takes its log-sum-exp in 64 bits and
-//          its K best from its parts, one wave the K best of all by rank, and all
-//          copy the chosen states.
+//   rows     one wave per part of a beam's row of logits reads it once, in steps of
+//            64 vectors of 16 bytes: it sums the exponentials and collects the
+//            values above a bound that K values of earlier steps reach (at first
+//            the K best lanes of the first steps), and raises the bound whenever
+//            its list is full.  A part whose list overflows by itself (long runs
+//            of equal or rising logits) or holds fewer than K finite values is
+//            read again and its K best are extracted one by one.
+//   join     one sentence per workgroup: a wave per beam takes its log-sum-exp in
+//            64 bits and its K best from its parts; then each of the K*K proposals
+//            counts those that precede it.
+//   states   a wave per state row copies the chosen beams' states (where they are
+//            few, the join does).
 //
 // The order of every sum and every comparison is by index in the row, never by
 // address: beams with equal rows get equal sums, and their ties stay ties.
@@ -29,6 +30,7 @@ namespace {
 constexpr int kMaxK = 16;
 constexpr int kMaxParts = 64;
 constexpr int kVecsPerLane = 64;  // of one part: an extraction rereads one lane's with one load
+constexpr int kCopyBytes = 16384; // states of a sentence that the join copies
 constexpr int kMaxV = 1 << 20;    // kMaxParts * 64 * kVecsPerLane vectors of four values
 
 struct BeamParams {
@@ -46,7 +48,7 @@ struct BeamParams {
   float alpha;
   long long stride;      // elements between rows
   int parts, vecs;       // parts of a row, 16-byte vectors of a part
-  int copies;            // workgroups per sentence of the join
+  int copy;              // the join copies the states
   int vec_copy;          // state rows are whole aligned 16-byte vectors
   double* part_sum;      // [B*K][parts]
   float* part_m;         // [B*K][parts]
@@ -164,28 +166,28 @@ __device__ __forceinline__ void Row<false>::load(const void* base, int i, int n,
   load_row<Row<false>>(base, i, n, pad, x);
 }
 
-// log2(e) as a sum of two floats
-constexpr float kL2eHi = 1.44268798828125f;
-constexpr float kL2eLo = 7.052607713387005e-06f;
+constexpr float kL2e = 1.44269504088896340736f;
 constexpr float kLowest = -3.402823466e38f;
+constexpr int kAhead = 4;   // steps in flight
+constexpr int kList = 64;   // values collected before the bound is raised: one a lane
 
-// Exponentials are taken in fp32 (v_exp_f32, one step) of the difference to a
-// reference value X that the lane has seen, summed over one vector in fp32 and
-// beyond that in 64 bits.  X follows the maximum only when that is 16 ahead, so
-// nearly never after the first vector.
-constexpr int kAhead = 4;   // vectors in flight per lane
-constexpr int kKept = 64;   // values kept by a part's second look
-
-// The K best of a part when more than kKept values reach the bound (long runs of
-// equal logits): extracted one by one, each from the lane whose next value comes
-// first, whose vectors (64 at most, one per lane) are reread.
+// The K best of a part, extracted one by one: each from the lane whose next value
+// comes first in the order (value falling, index rising), whose vectors (64 at
+// most, one per lane) are reread.
 template <bool BF>
-__device__ __noinline__ void part_best_by_one(const BeamParams& p, const char* base, int v0, int v1, float best,
-                                              int at, long long out) {
+__device__ __forceinline__ void part_best_by_one(const BeamParams& p, const char* base, int v0, int v1, int lane,
+                                                 long long out) {
   constexpr int VE = Row<BF>::VE;
-  const int lane = threadIdx.x & 63;
-  float last_v = INFINITY;
-  int last_i = -1;
+  float best = -INFINITY, last_v = INFINITY;
+  int at = v0 + lane < v1 ? v0 + lane : INT_MAX, last_i = -1;
+  for (int v = v0 + lane; v < v1; v += 64) {
+    float x[VE];
+    Row<BF>::load(base, v * VE, p.V, -INFINITY, x);
+    float mx = x[0];
+#pragma unroll
+    for (int j = 1; j < VE; ++j) mx = fmaxf(mx, x[j]);
+    if (mx > best) best = mx, at = v;
+  }
   for (int r = 0; r < p.K; ++r) {
     const int w = wave_best(best, at);
     const float lv = lane_f(last_v, w);
@@ -232,135 +234,192 @@ __device__ __noinline__ void part_best_by_one(const BeamParams& p, const char* b
   }
 }
 
-template <bool BF>
-__global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
-  constexpr int VE = Row<BF>::VE;
-  __shared__ float kept_v[4][kKept];
-  __shared__ int kept_i[4][kKept];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const long long job = (long long)blockIdx.x * 4 + wave;
-  const int row = (int)(job / p.parts), part = (int)(job % p.parts);
-  if (row >= p.B * p.K || p.finished[row]) return;
-  const char* base = static_cast<const char*>(p.logits) + (long long)row * p.stride * (BF ? 2 : 4);
-  const int nv = (p.V + VE - 1) / VE;
-  const int v0 = part * p.vecs, v1 = min(nv, v0 + p.vecs);
-
-  float X = kLowest, best = -INFINITY;
-  int at = v0 + lane < v1 ? v0 + lane : INT_MAX;
-  double sum = 0.0;
-  auto take = [&](int v, const float (&x)[VE]) {
-    float mx = x[0];
-#pragma unroll
-    for (int j = 1; j < VE; ++j) mx = fmaxf(mx, x[j]);
-    if (mx > best) {
-      best = mx;
-      at = v;
-      if (mx > X + 16.f) {
-        sum *= exp((double)X - (double)mx);
-        X = mx;
-      }
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < VE; ++j) {
-      const float d = x[j] - X;
-      s += __builtin_amdgcn_exp2f(fmaf(d, kL2eHi, d * kL2eLo));
-    }
-    sum += (double)s;
-  };
-  int v = v0 + lane;
-  // whole vectors of the row, kAhead at a time
-  const int whole = min(v1, p.V / VE);
-  for (; v + 64 * (kAhead - 1) < whole; v += 64 * kAhead) {
-    typename Row<BF>::Raw u[kAhead];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) u[a] = Row<BF>::raw(base, (v + 64 * a) * VE);
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      float x[VE];
-      Row<BF>::split(u[a], x);
-      take(v + 64 * a, x);
-    }
-  }
-  for (; v < v1; v += 64) {
-    float x[VE];
-    Row<BF>::load(base, v * VE, p.V, -INFINITY, x);
-    take(v, x);
-  }
-  // the part's sum: lanes in a fixed order of pairs
-  const float Xw = wave_max(X);
-  double sw = sum * exp((double)X - (double)Xw);
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) sw += __shfl_xor(sw, o);
-  const long long out = (long long)row * p.parts + part;
-  if (lane == 0) {
-    p.part_sum[out] = sw;
-    p.part_m[out] = Xw;
-  }
-
-  // the K lanes whose bests come first, the last of them the bound
-  float bound = -INFINITY, hv = best;
-  int hi = at, lanes = 0, chosen = 0;
-  for (; chosen < p.K; ++chosen) {
-    const int w = wave_best(hv, hi);
-    if (__builtin_amdgcn_readlane(hi, w) == INT_MAX) {  // fewer lanes than K have values: all of theirs count
-      bound = -INFINITY;
-      break;
-    }
-    bound = lane_f(hv, w);
-    if (lane == chosen) lanes = w;
-    if (lane == w) hv = -INFINITY, hi = INT_MAX;
-  }
-  // their values that reach it
-  const int each = (v1 - v0 + 63) / 64, total = chosen * each;
-  int kept = 0;
-  for (int t = lane; t - lane < total; t += 64) {
-    const int w = __shfl(lanes, min(t / each, chosen - 1));
-    const int u = v0 + w + 64 * (t % each);
-    const bool in = t < total && u < v1;
-    float x[VE];
-    if (in)
-      Row<BF>::load(base, u * VE, p.V, NAN, x);
-    else
-#pragma unroll
-      for (int j = 0; j < VE; ++j) x[j] = NAN;
-    float mx = x[0];
-#pragma unroll
-    for (int j = 1; j < VE; ++j) mx = fmaxf(mx, x[j]);
-    if (!__any(mx >= bound)) continue;
-#pragma unroll
-    for (int j = 0; j < VE; ++j) {
-      const unsigned long long who = __ballot(x[j] >= bound);
-      if (x[j] >= bound) {
-        const int pos = kept + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
-                                                         __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-        if (pos < kKept) {
-          kept_v[wave][pos] = x[j];
-          kept_i[wave][pos] = u * VE + j;
-        }
-      }
-      kept += __popcll(who);
-    }
-  }
-  if (kept > kKept) {
-    part_best_by_one<BF>(p, base, v0, v1, best, at, out);
-    return;
-  }
+// A wave's own LDS accesses take effect in order; only the compiler has to keep them so.
+__device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
   __builtin_amdgcn_wave_barrier();
-  float cv = -INFINITY, ov = -INFINITY;
-  int ci = INT_MAX, oi = INT_MAX;
-  if (lane < kept) {
-    cv = kept_v[wave][lane];
-    ci = kept_i[wave][lane];
-  }
-  for (int r = 0; r < p.K; ++r) {
+}
+
+// The K best of a wave's list of n (at most 64), in order, to its front and to lanes 0 .. K-1.
+__device__ __forceinline__ void list_best(float* lv, int* li, int n, int K, int lane, float& ov, int& oi) {
+  wave_lds_fence();
+  float cv = -INFINITY;
+  int ci = INT_MAX;
+  if (lane < n) cv = lv[lane], ci = li[lane];
+  ov = -INFINITY, oi = INT_MAX;
+  for (int r = 0; r < K; ++r) {
     const int w = wave_best(cv, ci);
     const float ev = lane_f(cv, w);
     const int ei = __builtin_amdgcn_readlane(ci, w);
     if (lane == r) ov = ev, oi = ei;
     if (lane == w) cv = -INFINITY, ci = INT_MAX;
   }
+  wave_lds_fence();
+  if (lane < K) lv[lane] = ov, li[lane] = oi;
+  wave_lds_fence();
+}
+
+// Exponentials are taken in fp32 (v_exp_f32, one step) of the difference to a
+// reference X near the part's maximum, where differences are exact or small,
+// summed over one vector in fp32 and beyond that in 64 bits.  X moves only when a
+// value is 16 above it.  Bound by the reading of the logits.
+template <bool BF>
+__global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
+  constexpr int VE = Row<BF>::VE;
+  typedef typename Row<BF>::Raw Raw;
+  __shared__ float list_v[4][kList];
+  __shared__ int list_i[4][kList];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const long long job = (long long)blockIdx.x * 4 + wave;
+  const int row = (int)(job / p.parts), part = (int)(job % p.parts);
+  if (row >= p.B * p.K) return;
+  const char* base = static_cast<const char*>(p.logits) + (long long)row * p.stride * (BF ? 2 : 4);
+  const int nv = (p.V + VE - 1) / VE;
+  const int v0 = part * p.vecs, v1 = min(nv, v0 + p.vecs);
+  float* lv = list_v[wave];
+  int* li = list_i[wave];
+
+  // a step's vector; past the part or the row -inf
+  const int whole = min(v1, p.V / VE);
+  auto fetch = [&](int v, float (&x)[VE]) {
+    if (v < v1)
+      Row<BF>::load(base, v * VE, p.V, -INFINITY, x);
+    else
+#pragma unroll
+      for (int j = 0; j < VE; ++j) x[j] = -INFINITY;
+  };
+  auto max_of = [&](const float (&x)[VE]) {
+    float mx = x[0];
+#pragma unroll
+    for (int j = 1; j < VE; ++j) mx = fmaxf(mx, x[j]);
+    return mx;
+  };
+
+  // the first steps: the reference and the first bound
+  float first[kAhead][VE];
+  {
+    const int v = v0 + lane;
+    if (v0 + 64 * kAhead <= whole) {
+      Raw u[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) u[a] = Row<BF>::raw(base, (v + 64 * a) * VE);
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) Row<BF>::split(u[a], first[a]);
+    } else {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) fetch(v + 64 * a, first[a]);
+    }
+  }
+  if (p.finished[row]) return;  // read beside the first steps
+  float hv = max_of(first[0]);
+#pragma unroll
+  for (int a = 1; a < kAhead; ++a) hv = fmaxf(hv, max_of(first[a]));
+  float X = fmaxf(wave_max(hv), kLowest), bound = -INFINITY;
+  for (int r = 0; r < p.K; ++r) {
+    const int w = wave_best(hv, lane);
+    bound = lane_f(hv, w);
+    if (lane == w) hv = -INFINITY;
+  }
+
+  double sum = 0.0;
+  int kept = 0;
+  bool full = false;
+  // a step's values of at least `least`, and of at least the bound where that has
+  // been raised within the step: later values of its size come after the K that
+  // reached it
+  auto collect = [&](const float (&x)[VE], int v, float least) {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      unsigned long long who = __ballot(x[j] >= least);
+      if (who == 0 || full) continue;
+      if (kept + __popcll(who) > kList) {
+        float ov;
+        int oi;
+        list_best(lv, li, kept, p.K, lane, ov, oi);
+        if (kept >= p.K) least = bound = fmaxf(bound, lane_f(ov, p.K - 1));
+        kept = min(kept, p.K);
+        who = __ballot(x[j] >= least);
+        full = kept + __popcll(who) > kList;
+        if (full) continue;
+      }
+      if (x[j] >= least) {
+        const int pos = kept + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
+                                                         __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+        lv[pos] = x[j];
+        li[pos] = v * VE + j;
+      }
+      kept += __popcll(who);
+    }
+  };
+  auto add = [&](const float (&x)[VE]) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < VE; ++j) s += __builtin_amdgcn_exp2f((x[j] - X) * kL2e);
+    sum += (double)s;
+  };
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) {
+    const float least = fmaxf(bound, kLowest);
+    if (__any(max_of(first[a]) >= least)) collect(first[a], v0 + lane + 64 * a, least);
+    add(first[a]);
+  }
+  auto take = [&](const float (&x)[VE], int v) {
+    const float mx = max_of(x);
+    if (__any(mx > bound)) {
+      const float top = wave_max(mx);
+      if (top > X + 16.f) {
+        sum *= exp((double)X - (double)top);
+        X = top;
+      }
+      // the least value above the bound (finite: X has been one)
+      const int bits = __builtin_bit_cast(int, bound);
+      const float least = bound < kLowest ? kLowest
+                          : bound == 0.f  ? __builtin_bit_cast(float, 1)
+                                          : __builtin_bit_cast(float, bound > 0.f ? bits + 1 : bits - 1);
+      collect(x, v, least);
+    }
+    add(x);
+  };
+  int s = v0 + 64 * kAhead;  // the step's first vector
+  for (; s + 64 * kAhead <= whole; s += 64 * kAhead) {
+    Raw u[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) u[a] = Row<BF>::raw(base, (s + lane + 64 * a) * VE);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      float x[VE];
+      Row<BF>::split(u[a], x);
+      take(x, s + lane + 64 * a);
+    }
+  }
+  if (s < v1) {  // the last steps, together
+    float x[kAhead][VE];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) fetch(s + lane + 64 * a, x[a]);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) take(x[a], s + lane + 64 * a);
+    s += 64 * kAhead;
+    if (s < v1) {  // V is no multiple of a vector: one more
+      fetch(s + lane, x[0]);
+      take(x[0], s + lane);
+    }
+  }
+
+  // the part's sum: lanes in a fixed order of pairs
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
+  const long long out = (long long)row * p.parts + part;
+  if (lane == 0) {
+    p.part_sum[out] = sum;
+    p.part_m[out] = X;
+  }
+  if (full || kept < p.K) {
+    part_best_by_one<BF>(p, base, v0, v1, lane, out);
+    return;
+  }
+  float ov;
+  int oi;
+  list_best(lv, li, kept, p.K, lane, ov, oi);
   if (lane < p.K) {
     p.part_val[out * p.K + lane] = ov;
     p.part_idx[out * p.K + lane] = oi;
@@ -368,146 +427,139 @@ __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
 }
 
 // ---- join ---------------------------------------------------------------------
-constexpr int kJoinWaves = 4;
+// Row i of layer l of the states to row `from` of the sources, by n threads.
+__device__ __forceinline__ void copy_row(const BeamParams& p, int which, long long from, long long to, int at, int n) {
+  const int size = which ? 4 : p.h_size, bytes = p.H * size;
+  const char* src = (which ? p.c : p.h) + from * bytes;
+  char* dst = (which ? p.c_out : p.h_out) + to * bytes;
+  if (p.vec_copy) {
+    const int per = bytes / 16;
+    const u32x4_a4* from4 = reinterpret_cast<const u32x4_a4*>(src);
+    for (int i = at; i < per; i += 4 * n) {
+      u32x4_a4 x[4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a) x[a] = from4[min(i + a * n, per - 1)];
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+        if (i + a * n < per) reinterpret_cast<u32x4_a4*>(dst)[i + a * n] = x[a];
+    }
+  } else if (size == 4) {
+    for (int i = at; i < p.H; i += n) reinterpret_cast<uint32_t*>(dst)[i] = reinterpret_cast<const uint32_t*>(src)[i];
+  } else {
+    for (int i = at; i < p.H; i += n) reinterpret_cast<uint16_t*>(dst)[i] = reinterpret_cast<const uint16_t*>(src)[i];
+  }
+}
 
-__global__ void __launch_bounds__(kJoinWaves * 64) beam_join_kernel(BeamParams p) {
-  __shared__ float heads_v[kJoinWaves][kMaxParts * kMaxK];  // a beam's parts' best
-  __shared__ int heads_i[kJoinWaves][kMaxParts * kMaxK];
-  __shared__ float val[kMaxK][kMaxK];  // the beams' best, in order
-  __shared__ int idx[kMaxK][kMaxK];
-  __shared__ double lses[kMaxK], pens[kMaxK];
+// A wave per beam.
+__global__ void __launch_bounds__(kMaxK * 64) beam_join_kernel(BeamParams p) {
+  extern __shared__ char heads[];  // [K][parts * K] values, then indexes: a beam's parts' best
+  __shared__ double rank[kMaxK * kMaxK], cand[kMaxK * kMaxK];  // the beams' proposals, in order
+  __shared__ int tok[kMaxK * kMaxK];
   __shared__ int parent[kMaxK];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int b = blockIdx.x / p.copies, copy = blockIdx.x % p.copies;
-  const int K = p.K;
+  const int tid = threadIdx.x, lane = tid & 63, k = tid >> 6;
+  const int b = blockIdx.x, K = p.K, row = b * K + k, n = p.parts * K;
+  float* hv = reinterpret_cast<float*>(heads) + k * n;
+  int* hi = reinterpret_cast<int*>(heads) + (K + k) * n;
 
-  // log-sum-exp and K best of every beam: lane i holds part i's next value
-  for (int k = wave; k < K; k += kJoinWaves) {
-    const int row = b * K + k;
-    const bool fin = p.finished[row] != 0;
-    if (lane == 0) pens[k] = pow((5.0 + (p.lengths[row] + (fin ? 0 : 1))) / 6.0, (double)p.alpha);
-    if (fin) continue;
+  // log-sum-exp and K best of the beam: lane i holds part i's next value
+  const bool fin = p.finished[row] != 0;
+  const double score = p.scores[row];
+  const int length = p.lengths[row] + (fin ? 0 : 1);
+  float M = kLowest;
+  double s = 0.0;
+  if (!fin) {
     const long long at = (long long)row * p.parts;
-    float M = kLowest;
-    double s = 0.0;
     if (lane < p.parts) {
       M = p.part_m[at + lane];
       s = p.part_sum[at + lane];
     }
-    for (int i = lane; i < p.parts * K; i += 64) {
-      heads_v[wave][i] = p.part_val[at * K + i];
-      heads_i[wave][i] = p.part_idx[at * K + i];
+    for (int i = lane; i < n; i += 64) {
+      hv[i] = p.part_val[at * K + i];
+      hi[i] = p.part_idx[at * K + i];
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-    __builtin_amdgcn_wave_barrier();
+  }
+  const double pen = p.alpha == 0.f ? 1.0 : pow((5.0 + length) / 6.0, (double)p.alpha);
+  wave_lds_fence();
+  float ov = -INFINITY;  // lane r: the beam's r-th best
+  int oi = INT_MAX;
+  double lse = 0.0;
+  if (!fin) {
     const float Mw = wave_max(M);
     s *= exp((double)M - (double)Mw);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
     // no distribution: NaN or +inf among the logits, or all -inf
-    if (lane == 0) lses[k] = s > 0.0 && s < INFINITY ? (double)Mw + log(s) : (double)NAN;
+    lse = s > 0.0 && s < INFINITY ? (double)Mw + log(s) : (double)NAN;
     int j = 0, i = INT_MAX;
     float v = -INFINITY;
-    if (lane < p.parts) {
-      v = heads_v[wave][lane * K];
-      i = heads_i[wave][lane * K];
-    }
+    if (lane < p.parts) v = hv[lane * K], i = hi[lane * K];
     for (int r = 0; r < K; ++r) {
       const int w = wave_best(v, i);
+      const float ev = lane_f(v, w);
+      const int ei = __builtin_amdgcn_readlane(i, w);
+      if (lane == r) ov = ev, oi = ei;
       if (lane == w) {
-        val[k][r] = v;
-        idx[k][r] = i;
         const bool more = lane < p.parts && ++j < K;
-        v = more ? heads_v[wave][lane * K + j] : -INFINITY;
-        i = more ? heads_i[wave][lane * K + j] : INT_MAX;
+        v = more ? hv[lane * K + j] : -INFINITY;
+        i = more ? hi[lane * K + j] : INT_MAX;
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-    __builtin_amdgcn_wave_barrier();
   }
-  __syncthreads();
-
-  // the K best of all: lane k holds beam k's next proposal
-  if (wave == 0) {
-    const bool beam = lane < K;
-    const int k = beam ? lane : 0, row = b * K + k;
-    const bool fin = p.finished[row] != 0;
-    const double score = p.scores[row];
-    const int n = p.lengths[row] + (fin ? 0 : 1);
-    const double pen = pens[k], lse = fin ? 0.0 : lses[k];
+  if (lane < K) {
     // proposes rank -inf only
     const bool none = !(score > -INFINITY) || score == INFINITY || isnan(lse);
-    int j = 0, tok = 0;
-    double cand = -INFINITY, rank = -INFINITY;
-    auto next = [&]() {
-      if (!beam || j >= K) {
-        tok = INT_MAX, cand = rank = -INFINITY;
-        return;
-      }
-      if (none) {
-        tok = j, cand = -INFINITY;
-      } else if (fin) {
-        tok = j == 0 ? p.eos : (j - 1 < p.eos ? j - 1 : j);
-        cand = j == 0 ? score : -INFINITY;
-      } else {
-        tok = idx[k][j];
-        cand = score + ((double)val[k][j] - lse);
-      }
-      rank = cand / pen;
-    };
-    next();
-    for (int r = 0; r < K; ++r) {
-      // the largest rank, of equals the lowest beam (its next proposal precedes every other beam's token)
-      double br = rank;
-      int bk = tok != INT_MAX ? lane : INT_MAX;
-#pragma unroll
-      for (int o = 1; o < kMaxK; o <<= 1) {
-        const double orr = __shfl_xor(br, o);
-        const int ok = __shfl_xor(bk, o);
-        const bool better = ok != INT_MAX && (bk == INT_MAX || orr > br || (orr == br && ok < bk));
-        br = better ? orr : br;
-        bk = better ? ok : bk;
-      }
-      if (lane == bk) {
-        parent[r] = lane;
-        if (copy == 0) {
-          const int o = b * K + r;
-          p.tokens[o] = tok;
-          p.parents[o] = lane;
-          p.scores_out[o] = (float)cand;
-          p.finished_out[o] = fin || tok == p.eos;
-          p.lengths_out[o] = n;
-        }
-        ++j;
-        next();
-      }
+    int t;
+    double c = -INFINITY;
+    if (none) {
+      t = lane;
+    } else if (fin) {
+      t = lane == 0 ? p.eos : (lane - 1 < p.eos ? lane - 1 : lane);
+      if (lane == 0) c = score;
+    } else {
+      t = oi;
+      c = score + ((double)ov - lse);
     }
+    const double r = c / pen;
+    tok[k * K + lane] = t;
+    cand[k * K + lane] = c;
+    rank[k * K + lane] = isnan(r) ? -INFINITY : r;
   }
   __syncthreads();
 
-  // the chosen beams' states
-  const int part = copy * (kJoinWaves * 64) + tid, all = p.copies * (kJoinWaves * 64);
-  const long long BK = (long long)p.B * K;
-  for (int which = 0; which < 2; ++which) {
-    const char* src = which ? p.c : p.h;
-    char* dst = which ? p.c_out : p.h_out;
-    const int size = which ? 4 : p.h_size;
-    if (!src) continue;
-    const int unit = p.vec_copy ? 16 : size;
-    const int per = p.H * size / unit;  // units of one state row
-    const int n = p.L * K * per;
-    for (int i = part; i < n; i += all) {
-      const int u = i % per, lk = i / per, r = lk % K, l = lk / K;
-      const long long to = ((l * BK + (long long)b * K + r) * per + u) * unit;
-      const long long from = ((l * BK + (long long)b * K + parent[r]) * per + u) * unit;
-      if (unit == 16)
-        *reinterpret_cast<uint4*>(dst + to) = *reinterpret_cast<const uint4*>(src + from);
-      else if (unit == 4)
-        *reinterpret_cast<uint32_t*>(dst + to) = *reinterpret_cast<const uint32_t*>(src + from);
-      else
-        *reinterpret_cast<uint16_t*>(dst + to) = *reinterpret_cast<const uint16_t*>(src + from);
+  // Each proposal's place is the number of those before it: of a larger rank, or
+  // of an equal one from a lower beam or, in its own beam, further ahead.
+  if (tid < K * K) {
+    const double r = rank[tid];
+    int place = 0;
+    for (int i = 0; i < K * K; ++i) place += rank[i] > r || (rank[i] == r && i < tid);
+    if (place < K) {
+      const int from = tid / K, o = b * K + place;
+      const bool f = p.finished[b * K + from] != 0;
+      parent[place] = from;
+      p.tokens[o] = tok[tid];
+      p.parents[o] = from;
+      p.scores_out[o] = (float)cand[tid];
+      p.finished_out[o] = f || tok[tid] == p.eos;
+      p.lengths_out[o] = p.lengths[b * K + from] + (f ? 0 : 1);
     }
   }
+  if (!p.copy) return;
+  __syncthreads();
+  const long long BK = (long long)p.B * K;
+  for (int l = 0; l < p.L; ++l) {
+    if (p.h) copy_row(p, 0, l * BK + (long long)b * K + parent[k], l * BK + row, lane, 64);
+    if (p.c) copy_row(p, 1, l * BK + (long long)b * K + parent[k], l * BK + row, lane, 64);
+  }
+}
+
+// A wave per row of h and of c.
+__global__ void __launch_bounds__(256) beam_states_kernel(BeamParams p) {
+  const long long BK = (long long)p.B * p.K, job = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int which = p.h ? (p.c ? (int)(job & 1) : 0) : 1;
+  const long long at = p.h && p.c ? job >> 1 : job;
+  if (at >= p.L * BK) return;
+  const long long l = at / BK, r = at % BK;
+  copy_row(p, which, l * BK + r / p.K * p.K + p.parents[r], at, threadIdx.x & 63, 64);
 }
 
 // ---- host ---------------------------------------------------------------------
@@ -519,7 +571,8 @@ lstm_status_t check(const lstm_beam_desc_t* d) {
   if (d->L < 0 || d->H < 0 || (d->L == 0) != (d->H == 0)) return LSTM_ERR_INVALID_ARG;
   if (d->logits_stride != 0 && d->logits_stride < d->V) return LSTM_ERR_INVALID_ARG;
   if (d->K > kMaxK || d->V > kMaxV || (long long)d->B * d->K >= 1 << 24) return LSTM_ERR_UNSUPPORTED;
-  if ((long long)d->L * d->H * 16 * kMaxK >= 1ll << 31) return LSTM_ERR_UNSUPPORTED;
+  if ((long long)d->L * d->H * 16 * kMaxK >= 1ll << 31 || (long long)d->B * d->K * d->L >= 1ll << 31)
+    return LSTM_ERR_UNSUPPORTED;
   return LSTM_OK;
 }
 
@@ -591,12 +644,8 @@ lstm_status_t lstm_beam_step(const lstm_beam_desc_t* d, const void* logits, cons
   p.part_idx = (int*)at;
   p.vec_copy = (d->H * size) % 16 == 0 && (d->H * 4) % 16 == 0 && aligned(h, 16) && aligned(h_out, 16) &&
                aligned(c, 16) && aligned(c_out, 16);
-  // about 32 KiB of states a workgroup
   const long long state = (long long)d->L * d->K * d->H * ((h ? size : 0) + (c ? 4 : 0));
-  long long copies = state / 32768;
-  if (copies < 1) copies = 1;
-  if (copies > 64) copies = 64;
-  p.copies = (int)copies;
+  p.copy = state > 0 && state <= kCopyBytes;
 
   const long long blocks = ((long long)n + 3) / 4;
   if (d->dtype == LSTM_BF16)
@@ -604,8 +653,15 @@ lstm_status_t lstm_beam_step(const lstm_beam_desc_t* d, const void* logits, cons
   else
     hipLaunchKernelGGL((beam_rows_kernel<false>), dim3((unsigned)blocks), dim3(256), 0, stream, p);
   if (hipGetLastError() != hipSuccess) return LSTM_ERR_HIP;
-  hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)(d->B * p.copies)), dim3(256), 0, stream, p);
-  return hipGetLastError() == hipSuccess ? LSTM_OK : LSTM_ERR_HIP;
+  hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)d->B), dim3(d->K * 64), (size_t)p.parts * d->K * d->K * 8, stream,
+                     p);
+  if (hipGetLastError() != hipSuccess) return LSTM_ERR_HIP;
+  if (state > kCopyBytes) {
+    const long long jobs = (long long)d->L * d->B * d->K * ((h ? 1 : 0) + (c ? 1 : 0));
+    hipLaunchKernelGGL(beam_states_kernel, dim3((unsigned)((jobs + 3) / 4)), dim3(256), 0, stream, p);
+    if (hipGetLastError() != hipSuccess) return LSTM_ERR_HIP;
+  }
+  return LSTM_OK;
 }
 
 }  // extern "C"

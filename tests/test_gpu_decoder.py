@@ -368,3 +368,28 @@ def test_beam_steps_capture():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(first, outs)), i
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["rising", "falling", "few", "late", "blocks"])
+def test_beam_orders_of_logits(kind, dtype):
+    """What the single pass over a row has to raise its bound for, or to give up on."""
+    V = 40001
+    logits, scores, fin, lengths, h, c = beam_inputs(1, 4, V, dtype, seed=10, finished=0)
+    if kind in ("rising", "falling"):
+        x = logits.sort(-1, descending=kind == "falling").values
+    elif kind == "few":  # a vocabulary constrained to three tokens
+        x = torch.full_like(logits, -math.inf)
+        x[..., 5] = 1.0
+        x[..., 7] = 0.5
+        x[:, 1:, V - 1] = 2.0
+    elif kind == "late":  # the best at the row's end, far above the rest
+        x = logits.clone()
+        x[..., -3:] = torch.tensor([90.0, 91.0, 89.0]).to(x)
+    else:  # runs of equal values
+        x = (torch.arange(V) // 1000 % 7).to(logits).expand_as(logits).clone()
+    check_beam(x, scores, fin, lengths, h, c)
+
+
+def test_beam_of_many_parts():
+    check_beam(*beam_inputs(1, 16, 300001, "f32", seed=11, H=1024, L=2))
