@@ -259,10 +259,12 @@ __device__ __forceinline__ void list_best(float* lv, int* li, int n, int K, int 
   wave_lds_fence();
 }
 
-// Exponentials are taken in fp32 (v_exp_f32, one step) of the difference to a
-// reference X near the part's maximum, where differences are exact or small,
-// summed over one vector in fp32 and beyond that in 64 bits.  X moves only when a
-// value is 16 above it.  Bound by the reading of the logits.
+// Exponentials are taken in fp32 (v_exp_f32, one step) of one fused product
+// x * a - M, M the rounded a * X for a reference X near the part's maximum: exact
+// before its one rounding, so that the error is relative to the difference from
+// X.  They are summed over one vector in fp32 and beyond that in 64 bits; M's own
+// rounding is taken out of the sum at its end.  X moves only when a value is 16
+// above it.
 template <bool BF>
 __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
   constexpr int VE = Row<BF>::VE;
@@ -279,14 +281,22 @@ __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
   float* lv = list_v[wave];
   int* li = list_i[wave];
 
-  // a step's vector; past the part or the row -inf
+  // kAhead steps from vector s on: the reads, and a step's values, past the part or
+  // the row -inf
   const int whole = min(v1, p.V / VE);
-  auto fetch = [&](int v, float (&x)[VE]) {
-    if (v < v1)
-      Row<BF>::load(base, v * VE, p.V, -INFINITY, x);
-    else
+  auto fetch = [&](int s, Raw (&u)[kAhead]) {
+    if (whole <= v0) return;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) u[a] = Row<BF>::raw(base, min(s + lane + 64 * a, whole - 1) * VE);
+  };
+  auto values = [&](const Raw& u, int s, int a, float (&x)[VE]) {
+    Row<BF>::split(u, x);
+    const int v = s + lane + 64 * a;
+    if (s + 64 * (a + 1) > whole && v >= whole) {
 #pragma unroll
       for (int j = 0; j < VE; ++j) x[j] = -INFINITY;
+      if (v < v1) Row<BF>::load(base, v * VE, p.V, -INFINITY, x);
+    }
   };
   auto max_of = [&](const float (&x)[VE]) {
     float mx = x[0];
@@ -296,21 +306,13 @@ __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
   };
 
   // the first steps: the reference and the first bound
-  float first[kAhead][VE];
-  {
-    const int v = v0 + lane;
-    if (v0 + 64 * kAhead <= whole) {
-      Raw u[kAhead];
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) u[a] = Row<BF>::raw(base, (v + 64 * a) * VE);
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) Row<BF>::split(u[a], first[a]);
-    } else {
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) fetch(v + 64 * a, first[a]);
-    }
-  }
+  Raw u0[kAhead] = {}, u1[kAhead] = {};
+  fetch(v0, u0);
   if (p.finished[row]) return;  // read beside the first steps
+  if (v0 + 64 * kAhead < v1) fetch(v0 + 64 * kAhead, u1);
+  float first[kAhead][VE];
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) values(u0[a], v0, a, first[a]);
   float hv = max_of(first[0]);
 #pragma unroll
   for (int a = 1; a < kAhead; ++a) hv = fmaxf(hv, max_of(first[a]));
@@ -320,6 +322,9 @@ __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
     bound = lane_f(hv, w);
     if (lane == w) hv = -INFINITY;
   }
+  // where a * X could overflow, differences are 0 or beyond any exponent
+  auto by = [](float X) { return fabsf(X) < 1e37f ? kL2e : 1.f; };
+  float coef = by(X), M = coef * X;
 
   double sum = 0.0;
   int kept = 0;
@@ -354,9 +359,11 @@ __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
   auto add = [&](const float (&x)[VE]) {
     float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < VE; ++j) s += __builtin_amdgcn_exp2f((x[j] - X) * kL2e);
+    for (int j = 0; j < VE; ++j) s += __builtin_amdgcn_exp2f(fmaf(x[j], coef, -M));
     sum += (double)s;
   };
+  // the sum's factor to X
+  auto settle = [&]() { return exp2((double)M - (double)coef * (double)X); };
 #pragma unroll
   for (int a = 0; a < kAhead; ++a) {
     const float least = fmaxf(bound, kLowest);
@@ -366,12 +373,14 @@ __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
   auto take = [&](const float (&x)[VE], int v) {
     const float mx = max_of(x);
     if (__any(mx > bound)) {
-      const float top = wave_max(mx);
-      if (top > X + 16.f) {
-        sum *= exp((double)X - (double)top);
+      if (__any(mx > X + 16.f)) {
+        const float top = wave_max(mx);
+        sum *= settle() * exp((double)X - (double)top);
         X = top;
+        coef = by(X);
+        M = coef * X;
       }
-      // the least value above the bound (finite: X has been one)
+      // the least value above the bound
       const int bits = __builtin_bit_cast(int, bound);
       const float least = bound < kLowest ? kLowest
                           : bound == 0.f  ? __builtin_bit_cast(float, 1)
@@ -380,30 +389,22 @@ __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
     }
     add(x);
   };
-  int s = v0 + 64 * kAhead;  // the step's first vector
-  for (; s + 64 * kAhead <= whole; s += 64 * kAhead) {
-    Raw u[kAhead];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) u[a] = Row<BF>::raw(base, (s + lane + 64 * a) * VE);
+  auto batch = [&](const Raw (&u)[kAhead], int s) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       float x[VE];
-      Row<BF>::split(u[a], x);
+      values(u[a], s, a, x);
       take(x, s + lane + 64 * a);
     }
+  };
+  for (int s = v0 + 64 * kAhead; s < v1; s += 128 * kAhead) {
+    if (s + 64 * kAhead < v1) fetch(s + 64 * kAhead, u0);
+    batch(u1, s);
+    if (s + 64 * kAhead >= v1) break;
+    if (s + 128 * kAhead < v1) fetch(s + 128 * kAhead, u1);
+    batch(u0, s + 64 * kAhead);
   }
-  if (s < v1) {  // the last steps, together
-    float x[kAhead][VE];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) fetch(s + lane + 64 * a, x[a]);
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) take(x[a], s + lane + 64 * a);
-    s += 64 * kAhead;
-    if (s < v1) {  // V is no multiple of a vector: one more
-      fetch(s + lane, x[0]);
-      take(x[0], s + lane);
-    }
-  }
+  sum *= settle();
 
   // the part's sum: lanes in a fixed order of pairs
 #pragma unroll
