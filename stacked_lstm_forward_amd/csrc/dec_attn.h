@@ -49,7 +49,7 @@ struct AttnParams {
   float* part_o;         // nsplit > 1: [B*Hkv*rows][nsplit][D] unnormalised
   float* part_ml;        // [B*Hkv*rows][nsplit][2]: maximum (base-2 units) and sum
   float* stats;          // backward: [B*Hkv][rows][2], -lse (base-2 units) and -delta
-  int blocks_a;          // backward: workgroups that own keys
+  int rows_first, blocks_a;  // backward: workgroups that own rows go first; workgroups that go first
   int row_dg;            // backward: a tile of rows ahead, heads of the group and bytes of q and dout
   long long row_q0, row_q1, row_d0, row_d1;  // (.1: where the head passes the group's end)
 };
@@ -389,7 +389,9 @@ struct TileCopy {
       }
     }
   }
-  __device__ __forceinline__ void store(char* to, int s, int end, const uint8_t* mb, int tid, int db) {
+  // (`m` are the mask bytes of these rows, which another tensor's copy may have read)
+  __device__ __forceinline__ void store(char* to, int s, int end, const uint8_t* mb, int tid, int db,
+                                        const uint8_t (&m)[NV]) {
     if (s + KT > end) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)

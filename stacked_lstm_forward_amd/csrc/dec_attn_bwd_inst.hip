@@ -119,13 +119,14 @@ __device__ __forceinline__ void key_side(const AttnParams& p, int item, char* sm
   const int key0 = (tile * NW + wave) * 16 * C;
   const uint8_t* mb = p.key_mask ? p.key_mask + (long long)b * p.S : nullptr;
 
-  // a key left out is a key of zeros; its column of p is not used
+  // A key that the mask leaves out is read like any other: what it holds stays in
+  // its own column, which is not stored.
   uint4 kf[C][NCH], vf[C][NCH];
   auto left = [&](int s) { return s < keys && (!mb || mb[s]); };
 #pragma unroll
   for (int kc = 0; kc < C; ++kc) {
     const int s = key0 + kc * 16 + (lane & 15);
-    const bool ok = left(s);
+    const bool ok = s < keys;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       kf[kc][c] = load16(p.k + b * p.sk.b + s * p.sk.t + hk * p.sk.h, c * 64 + (lane >> 4) * 16, db, ok);
@@ -246,12 +247,12 @@ __device__ __forceinline__ void row_side(const AttnParams& p, int item, char* sm
   uint8_t rb = 0;
   auto load = [&](int s) {
     ck.load(s, keys, mb, tid, db);
-    cv.load(s, keys, mb, tid, db);
+    cv.load(s, keys, nullptr, tid, db);
     if (tid < KT) rb = s + tid < keys ? (mb ? mb[s + tid] : 1) : 0;
   };
   auto store = [&](int buf, int s) {
-    ck.store(sh.k[buf], s, keys, mb, tid, db);
-    cv.store(sh.v[buf], s, keys, mb, tid, db);
+    ck.store(sh.k[buf], s, keys, mb, tid, db, ck.m);
+    cv.store(sh.v[buf], s, keys, mb, tid, db, ck.m);
     if (tid < KT) sh.bias[buf][tid] = rb ? 0.f : -INFINITY;
   };
   if (keys > 0) {
@@ -303,10 +304,12 @@ __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(bwd_wav
 attn_bwd_kernel(AttnParams p) {
   __shared__ __align__(16) char smem[kShared];
   const int block = blockIdx.x;
-  if (block < p.blocks_a)
-    key_side(p, xcd_item(block, p.blocks_a), smem);
+  const bool first = block < p.blocks_a;
+  const int item = first ? xcd_item(block, p.blocks_a) : xcd_item(block - p.blocks_a, gridDim.x - p.blocks_a);
+  if (first != (p.rows_first != 0))
+    key_side(p, item, smem);
   else
-    row_side(p, xcd_item(block - p.blocks_a, gridDim.x - p.blocks_a), smem);
+    row_side(p, item, smem);
 }
 
 }  // namespace
@@ -321,8 +324,13 @@ hipError_t DEC_FN(DEC_BF16, DEC_DP)(const AttnParams& p0, hipStream_t s) {
   p.row_d0 = dt * p.sdo.t + p.row_dg * p.sdo.h, p.row_d1 = p.row_d0 + p.sdo.t - p.G * p.sdo.h;
   p.tiles = (p.rows + NW * 16 * C - 1) / (NW * 16 * C);
   p.kv_tiles = (p.S + NW * 16 * C - 1) / (NW * 16 * C);
-  p.blocks_a = p.B * p.Hkv * p.kv_tiles;
-  const long long n = (long long)p.blocks_a + (long long)p.B * p.Hkv * p.tiles;
+  // The row side, three products over the keys, goes first where its workgroups
+  // take twice as long as the key side's, four over the rows (32 x 200 rows, 777
+  // keys, D 80: 68 us, last 78); else last, where sentences that end early leave
+  // short workgroups (4 x 2048 rows, 3001 keys, D 128: 463 us, first 505).
+  p.rows_first = 3ll * p.S > 8ll * p.rows;
+  p.blocks_a = p.B * p.Hkv * (p.rows_first ? p.tiles : p.kv_tiles);
+  const long long n = (long long)p.B * p.Hkv * ((long long)p.tiles + p.kv_tiles);
   hipLaunchKernelGGL(attn_bwd_kernel, dim3((unsigned)n), dim3(NT), 0, s, p);
   return hipGetLastError();
 }

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
     if (tid < KT) rb = s + tid < s1 ? (mb ? mb[s + tid] : 1) : 0;
   };
   auto store_k = [&](int buf, int s) {
-    ck.store(skb[buf], s, s1, mb, tid, db);
+    ck.store(skb[buf], s, s1, mb, tid, db, ck.m);
     if (tid < KT) sbiasb[buf][tid] = rb ? 0.f : -INFINITY;
   };
   // -inf where a tile has keys left out
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
     cv.load(s0, s1, mb, tid, db);
     store_k(0, s0);
     if (s0 + KT < s1) load_k(s0 + KT);
-    cv.store(svb[0], s0, s1, mb, tid, db);
+    cv.store(svb[0], s0, s1, mb, tid, db, cv.m);
     if (s0 + KT < s1) store_k(1, s0 + KT);
     __syncthreads();
     mma_rows0<T, DP, QC, KT>(xa, skb[0], qf, lane);
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
     leave_out(y, s + KT, buf ^ 1);
     tile_max<QC, KT>(y, mn, p.scale_log2);
     if (more2) store_k(buf, s + 2 * KT);
-    if (more) cv.store(svb[buf ^ 1], s + KT, s1, mb, tid, db);
+    if (more) cv.store(svb[buf ^ 1], s + KT, s1, mb, tid, db, cv.m);
     __syncthreads();
   };
   for (int s = s0; s < s1; s += 2 * KT) {
