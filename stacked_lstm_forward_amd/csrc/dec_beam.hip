@@ -490,7 +490,9 @@ __global__ void __launch_bounds__(kMaxK * 64) beam_join_kernel(BeamParams p) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
     // no distribution: NaN or +inf among the logits, or all -inf
-    lse = s > 0.0 && s < INFINITY ? (double)Mw + log(s) : (double)NAN;
+    // (one lane's: the compiler may fuse a lane's own product into its sum, and
+    // equal logits must give equal ranks)
+    lse = __shfl(s > 0.0 && s < INFINITY ? (double)Mw + log(s) : (double)NAN, 0);
     int j = 0, i = INT_MAX;
     float v = -INFINITY;
     if (lane < p.parts) v = hv[lane * K], i = hi[lane * K];

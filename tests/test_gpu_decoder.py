@@ -393,3 +393,14 @@ def test_beam_orders_of_logits(kind, dtype):
 
 def test_beam_of_many_parts():
     check_beam(*beam_inputs(1, 16, 300001, "f32", seed=11, H=1024, L=2))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_beam_ties_far_apart_in_a_row(dtype):
+    """A beam's best values are equal and lie in different parts of its row: lowest index first."""
+    B, K, V = 40, 5, 32007
+    logits, scores, fin, lengths, h, c = beam_inputs(B, K, V, dtype, seed=12, finished=0)
+    g = torch.Generator().manual_seed(13)
+    at = torch.randint(3, V, (B, K, 4), generator=g).to(DEV)
+    logits.scatter_(2, at, 14.0)
+    check_beam(logits, scores, fin, lengths, h, c)
