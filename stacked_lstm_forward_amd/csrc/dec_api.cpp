@@ -20,6 +20,8 @@ typedef hipError_t (*AttnLaunch)(const AttnParams&, hipStream_t);
 const AttnLaunch kFwd[2][8] = {DEC_ROW(fwd, 0), DEC_ROW(fwd, 1)};
 const AttnLaunch kBwd[2][8] = {DEC_ROW(bwd, 0), DEC_ROW(bwd, 1)};
 #undef DEC_ROW
+const AttnLaunch kBwdNarrow[4] = {attn_bwd_narrow_launch_1_32, attn_bwd_narrow_launch_1_64,
+                                  attn_bwd_narrow_launch_1_96, attn_bwd_narrow_launch_1_128};
 
 constexpr long long kMaxCount = 1ll << 31;
 constexpr int kComputeUnits = 256;
@@ -161,7 +163,9 @@ lstm_status_t lstm_attn_bwd(const lstm_attn_desc_t* d, const void* q, const void
   p.stats = (float*)ws;
   const bool bf = d->dtype == LSTM_BF16;
   if (attn_stats_launch(p, bf, stream) != hipSuccess) return LSTM_ERR_HIP;
-  if (kBwd[bf][dp_index(d->D)](p, stream) != hipSuccess) return LSTM_ERR_HIP;
+  const int at = dp_index(d->D);
+  const AttnLaunch run = bwd_narrow(bf, (at + 1) * 32, p.rows, p.S) ? kBwdNarrow[at] : kBwd[bf][at];
+  if (run(p, stream) != hipSuccess) return LSTM_ERR_HIP;
   return LSTM_OK;
 }
 

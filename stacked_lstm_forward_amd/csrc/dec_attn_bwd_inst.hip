@@ -1,5 +1,6 @@
 // Attention over encoder outputs, gradients.  One translation unit per element
-// type and padded head size (DEC_BF16, DEC_DP).
+// type, padded head size (DEC_BF16, DEC_DP) and, where a wave's columns may be one
+// or two groups, choice of these (DEC_NARROW).
 //
 // One launch of two kinds of workgroups, each recomputing the probabilities from
 // q, k and lse: one kind owns keys and sums dk and dv over the rows, the other
@@ -29,12 +30,18 @@ typedef float ET;
 #endif
 constexpr int DP = DEC_DP;
 
-constexpr int C = bwd_columns(DEC_BF16, DEC_DP), NW = bwd_waves(DEC_BF16, DEC_DP), NT = NW * 64;
+#if DEC_NARROW
+constexpr int C = 1, NW = 4, RT = 32, KT = 32, kPerSimd = bwd_narrow_waves_per_simd(DEC_DP);
+constexpr bool kShort = false;
+#else
+constexpr int C = bwd_columns(DEC_BF16, DEC_DP), NW = bwd_waves(DEC_BF16, DEC_DP);
 constexpr int RT = bwd_row_tile(DEC_BF16, DEC_DP), KT = bwd_key_tile(DEC_BF16, DEC_DP);
+constexpr int kPerSimd = bwd_waves_per_simd(DEC_BF16, DEC_DP);
+constexpr bool kShort = bwd_short(DEC_BF16, DEC_DP);
+#endif
+constexpr int NT = NW * 64;
 constexpr int SZ = AT<ET>::SZ, PB = Pitch<ET, DP>::B;
 constexpr int NCH = DP * SZ / 64, VR = DP * SZ / 16, NTILES = DP / 16;
-constexpr bool kShort = bwd_short(DEC_BF16, DEC_DP);
-
 // LDS: two buffers each, a tile is written while its predecessor is read.
 struct KeySide {
   char q[2][RT * PB], d[2][RT * PB];
@@ -309,7 +316,7 @@ __device__ __forceinline__ void row_side(const AttnParams& p, int item, char* sm
   }
 }
 
-__global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(bwd_waves_per_simd(DEC_BF16, DEC_DP))))
+__global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(kPerSimd)))
 attn_bwd_kernel(AttnParams p) {
   __shared__ __align__(16) char smem[kShared];
   const int block = blockIdx.x;
@@ -323,7 +330,11 @@ attn_bwd_kernel(AttnParams p) {
 
 }  // namespace
 
+#if DEC_NARROW
+#define DEC_FN2(bf, dp) attn_bwd_narrow_launch_##bf##_##dp
+#else
 #define DEC_FN2(bf, dp) attn_bwd_launch_##bf##_##dp
+#endif
 #define DEC_FN(bf, dp) DEC_FN2(bf, dp)
 hipError_t DEC_FN(DEC_BF16, DEC_DP)(const AttnParams& p0, hipStream_t s) {
   AttnParams p = p0;

@@ -20,6 +20,10 @@ DEC_ATTN_DECLARE(192)
 DEC_ATTN_DECLARE(224)
 DEC_ATTN_DECLARE(256)
 #undef DEC_ATTN_DECLARE
+hipError_t attn_bwd_narrow_launch_1_32(const AttnParams&, hipStream_t);
+hipError_t attn_bwd_narrow_launch_1_64(const AttnParams&, hipStream_t);
+hipError_t attn_bwd_narrow_launch_1_96(const AttnParams&, hipStream_t);
+hipError_t attn_bwd_narrow_launch_1_128(const AttnParams&, hipStream_t);
 
 hipError_t attn_combine_launch(const AttnParams&, bool bf16, hipStream_t);
 hipError_t attn_stats_launch(const AttnParams&, bool bf16, hipStream_t);
@@ -60,6 +64,14 @@ constexpr int bwd_registers(bool bf16, int dp) { return bwd_columns(bf16, dp) * 
 constexpr bool bwd_short(bool bf16, int dp) { return bf16 && bwd_registers(bf16, dp) >= 192; }
 constexpr int bwd_waves(bool bf16, int dp) { return bwd_short(bf16, dp) ? 8 : 4; }
 constexpr int bwd_waves_per_simd(bool bf16, int dp) { return bf16 || bwd_registers(bf16, dp) < 192 ? 2 : 1; }
+// One group where there are few rows and keys: more, smaller workgroups then hide
+// each other's latency (300 rows, 400 keys at most, 192 heads of 64: 47 us, 55 with
+// two; 40 and 50, 256 heads of 128: 13 and 19; 200 and 777, 128 heads of 80: 78 and
+// 72; 1000 and 1000, 64 heads of 64: 99 and 86).
+constexpr bool bwd_narrow(bool bf16, int dp, int rows, int S) {
+  return bwd_columns(bf16, dp) == 2 && rows <= 512 && S <= 512;
+}
+constexpr int bwd_narrow_waves_per_simd(int dp) { return dp <= 64 ? 4 : 3; }
 constexpr int bwd_row_tile(bool bf16, int dp) { return bf16 && dp <= 64 ? 64 : 32; }
 constexpr int bwd_key_tile(bool bf16, int dp) { return bf16 && dp <= 160 ? 64 : 32; }
 

@@ -82,6 +82,21 @@ def test_attention(shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(3, 300, 600, 4, 2, 24), (3, 270, 550, 4, 2, 64), (3, 530, 560, 1, 1, 80),
+                                   (3, 180, 600, 9, 3, 128), (3, 600, 520, 1, 1, 160)], ids=str)
+def test_attention_of_many_rows_and_keys(shape, dtype):
+    B, Tq, S = shape[:3]
+    q, k, v, do = tensors(*shape, dtype, seed=14)
+    n = torch.tensor([S, 0, S // 2 + 5], dtype=torch.int32)
+    m = torch.rand(B, S, generator=torch.Generator().manual_seed(15)) < 0.7
+    bad = torch.tensor([math.nan, math.inf, -math.inf])[torch.arange(S) % 3].to(DT[dtype])
+    check(q, k, v, do)
+    for x in (k, v):  # what the mask leaves out is never used
+        x.copy_(torch.where(m[:, :, None, None], x.cpu(), bad[None, :, None, None]))
+    check(q, k, v, do, kv_len=n.to(DEV), key_mask=m.to(DEV))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("layout", ["bth", "bht", "wide"])
 def test_attention_layouts(layout, dtype):
     q, k, v, do = tensors(2, 21, 77, 4, 2, 64, dtype, layout, seed=1)
