@@ -270,26 +270,21 @@ __global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
   }
 
   uint4 kf[KT / 16][NCH], rv[NV];
-  uint8_t mk[KT / 16], mx4[KT / 16][4], mv[NV];  // mask bytes of the k rows, the score rows, the v rows
+  uint8_t mask = 0;  // lane i < KT: the mask byte of the tile's key i, a bit of every lane's `bits` below
   auto load_k = [&](int s) {
 #pragma unroll
     for (int kt = 0; kt < KT / 16; ++kt) {
       const int r = s + kt * 16 + l15;
 #pragma unroll
       for (int c = 0; c < NCH; ++c) kf[kt][c] = load16(kb + r * p.sk.t, c * 64 + g * 16, db, r < s1);
-      if (mb) {
-        mk[kt] = r < s1 ? mb[r] : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx4[kt][i] = s + kt * 16 + 4 * g + i < s1 ? mb[s + kt * 16 + 4 * g + i] : 0;
-      }
     }
+    if (mb && lane < KT) mask = s + lane < s1 ? mb[s + lane] : 0;
   };
   auto load_v = [&](int s) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = lane + j * 64, r = s + i / VR;
       rv[j] = load16(vb + r * p.sv.t, (i % VR) * 16, db, r < s1);
-      if (mb) mv[j] = r < s1 ? mb[r] : 0;
     }
   };
   const int first = s0 + wave * KT;
@@ -299,17 +294,18 @@ __global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
   }
   for (int s = first; s < s1; s += NW * KT) {
     f32x4 x[KT / 16][QC];
+    const uint32_t bits = mb ? (uint32_t)__ballot(mask != 0) : 0xffffffffu;
 #pragma unroll
     for (int kt = 0; kt < KT / 16; ++kt) {
       f32x4 bias;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        bias[i] = s + kt * 16 + 4 * g + i < s1 && (!mb || mx4[kt][i]) ? 0.f : -INFINITY;
+        bias[i] = s + kt * 16 + 4 * g + i < s1 && (bits >> (kt * 16 + 4 * g + i) & 1) ? 0.f : -INFINITY;
 #pragma unroll
       for (int qc = 0; qc < QC; ++qc) x[kt][qc] = bias;
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
-        if (mb && !mk[kt]) kf[kt][c] = make_uint4(0, 0, 0, 0);
+        if (mb && !(bits >> (kt * 16 + l15) & 1)) kf[kt][c] = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int qc = 0; qc < QC; ++qc) mma_chunk<T>(x[kt][qc], kf[kt][c], qf[qc][c]);
       }
@@ -319,7 +315,7 @@ __global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = lane + j * 64;
-      if (mb && !mv[j]) rv[j] = make_uint4(0, 0, 0, 0);
+      if (mb && !(bits >> (i / VR) & 1)) rv[j] = make_uint4(0, 0, 0, 0);
       *reinterpret_cast<uint4*>(sv + (i / VR) * PB + (i % VR) * 16) = rv[j];
     }
     if (s + NW * KT < s1) load_v(s + NW * KT);
