@@ -29,9 +29,11 @@
  * recurrence's [T][B][H] outputs and [B][T][H] tensors are read in place.
  * The gradients have strides of their own.  lse [B][Hq][Tq] fp32, dense.
  * kv_len [B] int32, key_mask [B][S] bytes, dense.  Products take dtype operands
- * (p and dz rounded to dtype for theirs) and accumulate in fp32; softmax
- * statistics, lse and delta are fp32.  All sums are taken in a fixed order, so
- * results are deterministic.
+ * (bf16: p and dz enter theirs as the sum of two bf16 values, within 2^-16) and
+ * accumulate in fp32; softmax statistics, lse and delta are fp32 (delta is taken
+ * from the o that is handed in, rounded as it is).  An infinity in v at a key or in
+ * dout reaches o and the gradients as an infinity or NaN.  All sums are taken in a
+ * fixed order, so results are deterministic.
  *
  * Limits: D a multiple of 8, 8 ... 256; Hq a multiple of Hkv; every pointer
  * aligned to 16 bytes and every stride a multiple of 16 bytes; scale > 0 (0

@@ -7,7 +7,7 @@
 // Products.  Every kernel forms the scores transposed where its wave owns query
 // rows (S^T = K Q^T, "columns are queries") and untransposed where it owns keys
 // (S = Q K^T, "columns are keys"): either way the 16x16 output of one MFMA
-// (lane l: column l%16, rows 4*(l/16)+i) is, after the softmax and a rounding,
+// (lane l: column l%16, rows 4*(l/16)+i) is, after the softmax and the split below,
 // already the B operand of the next product, whose sum runs over those rows.
 // The order of a product's sum is free, so the k-slots of that operand are
 // taken as they lie: for bf16 (16x16x32) lane group g holds rows 4g..4g+3 of two
@@ -152,23 +152,24 @@ __device__ __forceinline__ s16x4 lds_tr4(const char* p) {
       (__attribute__((address_space(3))) s16x4*)(p));
 }
 
-// acc[n][qc] += tile(rows ROW0 .., transposed) * b[..][qc] for all column tiles n.
-// bf16: p[0][qc], p[1][qc] are the packed values of two 16-row tiles.
+// acc[n][qc] += tile(32 rows, transposed) * (hi + lo)[..][qc] for all column tiles n;
+// hi and lo hold the packed values of two 16-row tiles.
 template <typename T, int DP, int QC, int NTILES>
-__device__ __forceinline__ void mma_tr_bf16(f32x4 (&acc)[NTILES][QC], const char* tile, const uint2 (&p0)[QC],
-                                            const uint2 (&p1)[QC], int lane) {
+__device__ __forceinline__ void mma_tr_bf16(f32x4 (&acc)[NTILES][QC], const char* tile, const uint4 (&hi)[QC],
+                                            const uint4 (&lo)[QC], int lane) {
   constexpr int PB = Pitch<T, DP>::B;
   const char* base = tile + (lane >> 2) * PB + (lane & 3) * 8;
 #pragma unroll
   for (int n = 0; n < NTILES; ++n) {
-    const s16x4 lo = lds_tr4(base + n * 32);
-    const s16x4 hi = lds_tr4(base + n * 32 + 16 * PB);
-    const s16x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    const s16x4 x = lds_tr4(base + n * 32);
+    const s16x4 y = lds_tr4(base + n * 32 + 16 * PB);
+    const bf16x8 a = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
     for (int qc = 0; qc < QC; ++qc) {
-      const uint4 b = make_uint4(p0[qc].x, p0[qc].y, p1[qc].x, p1[qc].y);
-      acc[n][qc] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                           __builtin_bit_cast(bf16x8, b), acc[n][qc], 0, 0, 0);
+      acc[n][qc] =
+          __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, hi[qc]), acc[n][qc], 0, 0, 0);
+      acc[n][qc] =
+          __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, lo[qc]), acc[n][qc], 0, 0, 0);
     }
   }
 }
@@ -203,8 +204,22 @@ __device__ __forceinline__ void mma_tr_f32(f32x4 (&acc)[NTILES][QC], const char*
   }
 }
 
+// x and y less the rounded values that u holds
+__device__ __forceinline__ uint32_t rest_bf16(float x, float y, uint32_t u) {
+  return pack_bf16(x - bf16_lo(u), y - bf16_hi(u));
+}
+
 // acc += (rows of `tile`, KT of them, transposed) * p, p in score layout
-// [KT/16][QC] (fp32; rounded to bf16 here for bf16 products).
+// [KT/16][QC], fp32.  For bf16 products p is the sum of two bf16 values, its
+// rounding and the rounding of what that leaves (together within 2^-16 of p), and
+// each takes a product of its own.  One rounding of p (2^-8) would add an error as
+// large as the outputs' own rounding: 2-norm errors of o, dq, dk, dv against 64 bits
+// 0.0023, 0.0024-0.0025, 0.0024, 0.0023 instead of 0.0017, 0.0017-0.0018, 0.0017,
+// 0.0017 (fp32 products and a last rounding: 0.0017).  The second product costs
+// nothing where reading k and v is the bound (16 x 8 rows, 32768 keys: 384 us either
+// way), 15 % where latency is (64 x 200 rows, 331 keys: 16.3 and 19.0 us) and 25 to
+// 29 % of the longest cases (8 x 2048 rows, 4096 keys, 32 heads of 128: 1.22 and 1.54
+// ms; its training step with 4 x 2048 rows, 3001 keys, 12 heads: 599 and 771 us).
 template <typename T, int DP, int QC, int KT, int NTILES>
 __device__ __forceinline__ void mma_tr(f32x4 (&acc)[NTILES][QC], const char* tile, const f32x4 (&p)[KT / 16][QC],
                                        int lane) {
@@ -212,14 +227,17 @@ __device__ __forceinline__ void mma_tr(f32x4 (&acc)[NTILES][QC], const char* til
   if constexpr (AT<T>::BF) {
 #pragma unroll
     for (int ks = 0; ks < KT / 32; ++ks) {
-      uint2 p0[QC], p1[QC];
+      uint4 hi[QC], lo[QC];
 #pragma unroll
       for (int qc = 0; qc < QC; ++qc) {
         const f32x4 x = p[2 * ks][qc], y = p[2 * ks + 1][qc];
-        p0[qc] = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-        p1[qc] = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+        const uint4 h = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(y[0], y[1]),
+                                   pack_bf16(y[2], y[3]));
+        hi[qc] = h;
+        lo[qc] = make_uint4(rest_bf16(x[0], x[1], h.x), rest_bf16(x[2], x[3], h.y), rest_bf16(y[0], y[1], h.z),
+                            rest_bf16(y[2], y[3], h.w));
       }
-      mma_tr_bf16<T, DP, QC, NTILES>(acc, tile + ks * 32 * PB, p0, p1, lane);
+      mma_tr_bf16<T, DP, QC, NTILES>(acc, tile + ks * 32 * PB, hi, lo, lane);
     }
   } else {
 #pragma unroll
