@@ -53,8 +53,12 @@
  *     finished_out = finished[b,parent] or token == eos
  * and the states of the chosen beams: for n_states layers,
  *     h_out[l, b*K + i] = h[l, b*K + parents[b,i]] ,  c likewise.
- * The log-sum-exp, cand and rank are computed in 64 bits, since proposals of
- * different beams may lie closer together than fp32 tells apart.
+ * cand and rank are computed in 64 bits, since proposals of different beams may
+ * lie closer together than fp32 tells apart.  The log-sum-exp takes the largest
+ * logits' exponentials and all sums beyond 8 values in 64 bits, the other
+ * exponentials in fp32: it is within 2^-19 at worst (every rounding one way), 2^-26
+ * to 2^-29 for logits of a normal distribution, and proposals of different beams
+ * that lie closer together than that may change places.  cand is at most scores[b,k].
  *
  * Layouts: logits [B][K][V] dtype, dense rows of V with beam stride
  * logits_stride (elements, 0 selects V); scores, scores_out [B][K] fp32;

@@ -166,7 +166,9 @@ __device__ __forceinline__ void Row<false>::load(const void* base, int i, int n,
   load_row<Row<false>>(base, i, n, pad, x);
 }
 
-constexpr float kL2e = 1.44269504088896340736f;
+constexpr double kLog2e = 1.44269504088896340736;
+constexpr float kL2e = (float)kLog2e;
+constexpr double kTail = 1.0 - (double)kL2e / kLog2e;  // what the rounded factor takes from an exponent
 constexpr float kLowest = -3.402823466e38f;
 constexpr int kAhead = 4;   // steps in flight
 constexpr int kList = 64;   // values collected before the bound is raised: one a lane
@@ -241,9 +243,10 @@ __device__ __forceinline__ void wave_lds_fence() {
 }
 
 // The K best of a wave's list of n (at most 64), in order, to its front and to lanes 0 .. K-1.
-__device__ __forceinline__ void list_best(float* lv, int* li, int n, int K, int lane, float& ov, int& oi) {
+// `cv` is what is left of the list: a value a lane, -inf where there is none.
+__device__ __forceinline__ void list_best(float* lv, int* li, int n, int K, int lane, float& ov, int& oi, float& cv) {
   wave_lds_fence();
-  float cv = -INFINITY;
+  cv = -INFINITY;
   int ci = INT_MAX;
   if (lane < n) cv = lv[lane], ci = li[lane];
   ov = -INFINITY, oi = INT_MAX;
@@ -259,14 +262,22 @@ __device__ __forceinline__ void list_best(float* lv, int* li, int n, int K, int 
   wave_lds_fence();
 }
 
-// Exponentials are taken in fp32 (v_exp_f32, one step) of one fused product
-// x * a - M, M the rounded a * X for a reference X near the part's maximum: exact
-// before its one rounding, so that the error is relative to the difference from
-// X.  They are summed over one vector in fp32 and beyond that in 64 bits; M's own
-// rounding is taken out of the sum at its end.  X moves only when a value is 16
-// above it.
+// The sum.  Values that enter the list are the largest so far; their exponentials
+// are taken in 64 bits when they leave it.  The others' are taken in fp32
+// (v_exp_f32, one step) of one fused product x * a - M, M the rounded a * X for a
+// reference X at most 1 below the largest value: exact before its one rounding, so
+// that the error is relative to the difference from X.  They are summed over one
+// vector in fp32 and beyond that in 64 bits.  M's own rounding and the first-order
+// effect of a's (kTail times the sum's mean difference from X, a vector's maximum
+// standing for its values) are taken out of the sum at its end.  Together within
+// 2^-19 of the sum if every rounding of the fp32 part went the same way, in which
+// case the proposals of beams closer than that could change places; normal logits of
+// deviation 0.5 to 5 leave 2^-26 (1000 values) to 2^-29 (131072); where the listed
+// values hold nearly all of the sum, it is as exact as 64 bits.  All exponentials in
+// fp32, with X up to 16 below the largest value, took 122 instead of 131 us (below)
+// and left up to 2^-20.
 //
-// 2048 rows of 131072 bf16 values, 85 % of them read: 124 us, 3.7 TB/s; vector
+// 2048 rows of 131072 bf16 values, 85 % of them read: 131 us, 3.5 TB/s; vector
 // instructions take about 70 % of that time (eight exponentials at a quarter of the
 // rate per vector, and the list).  320 rows of 32007: 15 us, latency: a wave has
 // nine steps, and its list to sort.  Keeping vectors instead of values in the list
@@ -334,27 +345,30 @@ __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
   auto by = [](float X) { return fabsf(X) < 1e37f ? kL2e : 1.f; };
   float coef = by(X), M = coef * X;
 
-  double sum = 0.0;
+  double sum = 0.0, exact = 0.0;  // in units of 2^M, and of exp(X)
+  float tilt = 0.f;               // sum of exponentials times their vectors' differences from X
   int kept = 0;
   bool full = false;
   // a step's values of at least `least`, and of at least the bound where that has
   // been raised within the step: later values of its size come after the K that
-  // reached it
-  auto collect = [&](const float (&x)[VE], int v, float least) {
+  // reached it.  Their exponentials become 0.
+  auto collect = [&](const float (&x)[VE], int v, float least, float (&e)[VE]) {
 #pragma unroll
     for (int j = 0; j < VE; ++j) {
       unsigned long long who = __ballot(x[j] >= least);
       if (who == 0 || full) continue;
       if (kept + __popcll(who) > kList) {
-        float ov;
+        float ov, rest;
         int oi;
-        list_best(lv, li, kept, p.K, lane, ov, oi);
+        list_best(lv, li, kept, p.K, lane, ov, oi, rest);
+        sum += (double)__builtin_amdgcn_exp2f(fmaf(rest, coef, -M));
         if (kept >= p.K) least = bound = fmaxf(bound, lane_f(ov, p.K - 1));
         kept = min(kept, p.K);
         who = __ballot(x[j] >= least);
         full = kept + __popcll(who) > kList;
         if (full) continue;
       }
+      e[j] = x[j] >= least ? 0.f : e[j];
       if (x[j] >= least) {
         const int pos = kept + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
                                                          __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
@@ -364,38 +378,51 @@ __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
       kept += __popcll(who);
     }
   };
-  auto add = [&](const float (&x)[VE]) {
+  auto exponentials = [&](const float (&x)[VE], float (&e)[VE]) {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) e[j] = __builtin_amdgcn_exp2f(fmaf(x[j], coef, -M));
+  };
+  auto add = [&](const float (&e)[VE], float mx) {
     float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < VE; ++j) s += __builtin_amdgcn_exp2f(fmaf(x[j], coef, -M));
+    for (int j = 0; j < VE; ++j) s += e[j];
     sum += (double)s;
+    tilt = fmaf(s, fmaxf(mx - X, -128.f), tilt);  // (s is 0 before that)
   };
-  // the sum's factor to X
-  auto settle = [&]() { return exp2((double)M - (double)coef * (double)X); };
+  // the fp32 part in units of exp(X)
+  auto settled = [&]() { return (sum + kTail * (double)tilt) * exp2((double)M - (double)coef * (double)X); };
 #pragma unroll
   for (int a = 0; a < kAhead; ++a) {
     const float least = fmaxf(bound, kLowest);
-    if (__any(max_of(first[a]) >= least)) collect(first[a], v0 + lane + 64 * a, least);
-    add(first[a]);
+    const float mx = max_of(first[a]);
+    float e[VE];
+    exponentials(first[a], e);
+    if (__any(mx >= least)) collect(first[a], v0 + lane + 64 * a, least, e);
+    add(e, mx);
   }
   auto take = [&](const float (&x)[VE], int v) {
     const float mx = max_of(x);
+    float e[VE];
+    exponentials(x, e);
     if (__any(mx > bound)) {
-      if (__any(mx > X + 16.f)) {
+      if (__any(mx > X + 1.f)) {
         const float top = wave_max(mx);
-        sum *= settle() * exp((double)X - (double)top);
+        exact = (exact + settled()) * exp((double)X - (double)top);
+        sum = 0.0;
+        tilt = 0.f;
         X = top;
         coef = by(X);
         M = coef * X;
+        exponentials(x, e);
       }
       // the least value above the bound
       const int bits = __builtin_bit_cast(int, bound);
       const float least = bound < kLowest ? kLowest
                           : bound == 0.f  ? __builtin_bit_cast(float, 1)
                                           : __builtin_bit_cast(float, bound > 0.f ? bits + 1 : bits - 1);
-      collect(x, v, least);
+      collect(x, v, least, e);
     }
-    add(x);
+    add(e, mx);
   };
   auto batch = [&](const Raw (&u)[kAhead], int s) {
 #pragma unroll
@@ -412,23 +439,25 @@ __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
     if (s + 128 * kAhead < v1) fetch(s + 128 * kAhead, u1);
     batch(u0, s + 64 * kAhead);
   }
-  sum *= settle();
+  wave_lds_fence();
+  if (lane < kept) exact += exp((double)lv[lane] - (double)X);
+  exact += settled();
 
   // the part's sum: lanes in a fixed order of pairs
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
+  for (int o = 1; o < 64; o <<= 1) exact += __shfl_xor(exact, o);
   const long long out = (long long)row * p.parts + part;
   if (lane == 0) {
-    p.part_sum[out] = sum;
+    p.part_sum[out] = exact;
     p.part_m[out] = X;
   }
   if (full || kept < p.K) {
     part_best_by_one<BF>(p, base, v0, v1, lane, out);
     return;
   }
-  float ov;
+  float ov, rest;
   int oi;
-  list_best(lv, li, kept, p.K, lane, ov, oi);
+  list_best(lv, li, kept, p.K, lane, ov, oi, rest);
   if (lane < p.K) {
     p.part_val[out * p.K + lane] = ov;
     p.part_idx[out * p.K + lane] = oi;
@@ -509,6 +538,7 @@ __global__ void __launch_bounds__(kMaxK * 64) beam_join_kernel(BeamParams p) {
       const int w = wave_best(v, i);
       const float ev = lane_f(v, w);
       const int ei = __builtin_amdgcn_readlane(i, w);
+      if (r == 0 && lse < ev) lse = ev;  // no probability above 1
       if (lane == r) ov = ev, oi = ei;
       if (lane == w) {
         const bool more = lane < p.parts && ++j < K;

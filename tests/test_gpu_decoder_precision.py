@@ -1,8 +1,11 @@
-"""How exact the attention's 16-bit products are: p and dz enter them with 16 bits, not 8.
+"""How exact the decoder operators are, against the plain 64-bit forms.
 
-Bounds against the plain 64-bit forms, element by element: the output's own rounding (u = eps / 2 of the
-type), 2^-16 of p or dz for their two-part products, the fp32 arithmetic (as in ``decoder_reference``),
-and for dq and dk the rounding of the o that delta is taken from.
+Attention in bf16: p and dz enter their products with 16 bits, not 8.  Bounds, element by element: the
+output's own rounding (u = eps / 2 of the type), 2^-16 of p or dz for their two-part products, the fp32
+arithmetic (as in ``decoder_reference``), and for dq and dk the rounding of the o that delta is taken from.
+
+Beam search: the largest logits' exponentials count in 64 bits, the others' share of the sum in fp32 (all
+roundings one way, that share is off by 2^-19 of itself).
 """
 import math
 
@@ -11,7 +14,8 @@ import torch
 
 from stacked_lstm_forward_amd import decoder
 
-from .test_gpu_decoder import tensors, within
+from .decoder_reference import beam
+from .test_gpu_decoder import DEV, DT, beam_inputs, check_beam, tensors, within
 
 pytestmark = pytest.mark.gpu
 U = torch.finfo(torch.bfloat16).eps / 2
@@ -64,3 +68,47 @@ def test_products_hold_p_and_dz_in_sixteen_bits(shape):
     p.backward(do)
     for name, want in bounds(q, k, v, do).items():
         within(getattr(p, name), want, name)
+
+
+# ---- beam search ---------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("above", [1.5, 8.0, 12.0, 14.5, 15.75])
+def test_beam_log_probability_of_a_late_peak(above, dtype):
+    """One logit near the row's end, `above` the largest of those before it."""
+    B, K, V = 6, 3, 20000
+    logits, scores, fin, lengths, _, _ = beam_inputs(B, K, V, dtype, seed=31, finished=0)
+    g = torch.Generator().manual_seed(32)
+    x = torch.randn(B, K, V, generator=g).clamp(max=4.0)
+    x[..., V - 5] = 4.0 + above + torch.rand(B, K, generator=g) / 8
+    logits.copy_(x.to(DT[dtype]))
+    scores.copy_(torch.tensor([0.0, -9.0, -8.0]))
+    s = decoder.prepare_beam(logits, scores, fin, lengths, eos=2, alpha=0.0)
+    s.step()
+    want = beam(logits, scores, fin, lengths, 2, 0.0)[0]["scores"][:, 0]
+    got = s.scores_out.cpu().double()[:, 0]
+    assert s.tokens[:, 0].tolist() == [V - 5] * B and bool((got <= 0).all())
+    rest = -torch.expm1(want)  # the other logits' share of the sum
+    assert bool(((got - want).abs() <= 2.0 ** -19 * rest + 2.0 ** -24 * want.abs() + 1e-13).all())
+
+
+def near_ties(dtype):
+    """Every beam's best proposal ranks the same but for the rounding of its score, some 1e-8."""
+    B, K, V = 32, 4, 3000
+    logits, scores, fin, lengths, h, c = (t.cpu() for t in beam_inputs(B, K, V, dtype, seed=33, finished=0))
+    g = torch.Generator().manual_seed(34)
+    x = torch.randn(B, K, V, generator=g) - 70.0
+    at = torch.rand(B, K, V, generator=g).argsort(-1)[..., :3]
+    x.scatter_(-1, at, torch.rand(B, K, 3, generator=g) * torch.tensor([1.0, 1.0, 0.0]) + torch.tensor([0.0, 0.0, 2.0]))
+    logits.copy_(x.to(DT[dtype]))
+    d = logits.double()
+    scores.copy_((torch.logsumexp(d, -1) - d.amax(-1) - 0.01).float())
+    lengths.fill_(7)
+    return logits, scores, fin, lengths, h, c
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_beam_proposals_closer_than_fp32_tells_apart(dtype):
+    # three logits hold all of each sum: the log-sum-exp is as exact as 64 bits
+    check_beam(*(t.to(DEV) for t in near_ties(dtype)), gap=1e-13)
