@@ -23,7 +23,9 @@ const AttnLaunch kBwd[2][8] = {DEC_ROW(bwd, 0), DEC_ROW(bwd, 1)};
 const AttnLaunch kBwdNarrow[4] = {attn_bwd_narrow_launch_1_32, attn_bwd_narrow_launch_1_64,
                                   attn_bwd_narrow_launch_1_96, attn_bwd_narrow_launch_1_128};
 
-constexpr long long kMaxCount = 1ll << 31;
+// Lengths and row counts are held in 32 bits, and the kernels' counters step past
+// them by less than 4096 (two tiles of all waves).
+constexpr long long kMaxCount = (1ll << 31) - 4096;
 constexpr int kComputeUnits = 256;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -48,11 +50,10 @@ lstm_status_t check_desc(const lstm_attn_desc_t* d, bool train) {
                 !stride_ok(d->dv, size)))
     return LSTM_ERR_UNSUPPORTED;
   if (d->D % 8 != 0 || d->D > 256) return LSTM_ERR_UNSUPPORTED;
-  // counts the kernels and their grids hold in 32 bits
-  if ((long long)d->B * d->Hq >= kMaxCount || (long long)d->B * d->Hq * d->Tq >= kMaxCount ||
-      (long long)d->B * d->S >= kMaxCount)
+  if ((long long)d->B * d->Hq > kMaxCount || (long long)d->B * d->Hq * d->Tq > kMaxCount ||
+      (long long)d->B * d->S > kMaxCount)
     return LSTM_ERR_UNSUPPORTED;
-  const long long key_tiles = (d->S + 63) / 64 + 1;
+  const long long key_tiles = ((long long)d->S + 63) / 64 + 1;
   if ((long long)d->B * d->Hkv >= kMaxCount / key_tiles) return LSTM_ERR_UNSUPPORTED;
   return LSTM_OK;
 }

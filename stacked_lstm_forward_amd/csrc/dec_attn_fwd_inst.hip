@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
   const int db = p.D * SZ;
 
   const int s0 = split * p.kv_per_split;
-  const int s1 = min(keys_of(p, b), s0 + p.kv_per_split);
+  const int s1 = s0 + min(keys_of(p, b) - s0, p.kv_per_split);
   const char* kb = p.k + b * p.sk.b + hk * p.sk.h;
   const char* vb = p.v + b * p.sv.b + hk * p.sv.h;
   const uint8_t* mb = p.key_mask ? p.key_mask + (long long)b * p.S : nullptr;
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
   const int b = pair % p.B, hk = pair / p.B, bh = b * p.Hkv + hk;
   const int db = p.D * SZ;
   const int s0 = split * p.kv_per_split;
-  const int s1 = min(keys_of(p, b), s0 + p.kv_per_split);
+  const int s1 = s0 + min(keys_of(p, b) - s0, p.kv_per_split);
   const char* kb = p.k + b * p.sk.b + hk * p.sk.h;
   const char* vb = p.v + b * p.sv.b + hk * p.sv.h;
   const uint8_t* mb = p.key_mask ? p.key_mask + (long long)b * p.S : nullptr;
