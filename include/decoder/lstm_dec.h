@@ -37,8 +37,8 @@
  *
  * Limits: D a multiple of 8, 8 ... 256; Hq a multiple of Hkv; every pointer
  * aligned to 16 bytes and every stride a multiple of 16 bytes; scale > 0 (0
- * selects 1/sqrt(D)); B*Hq*Tq and B*S at most 2^31 - 4096.  Byte offsets are
- * 64-bit.
+ * selects 1/sqrt(D)); B*Hq*Tq and B*S at most 2^31 - 4096, for the gradients also
+ * B*Hkv*(ceil(Tq*Hq/(64*Hkv)) + ceil(S/64)).  Byte offsets are 64-bit.
  *
  * ---- beam search ----------------------------------------------------------
  * Sentence b holds K beams.  A beam that is not finished proposes every token v:

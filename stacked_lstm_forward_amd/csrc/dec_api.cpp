@@ -53,8 +53,9 @@ lstm_status_t check_desc(const lstm_attn_desc_t* d, bool train) {
   if ((long long)d->B * d->Hq > kMaxCount || (long long)d->B * d->Hq * d->Tq > kMaxCount ||
       (long long)d->B * d->S > kMaxCount)
     return LSTM_ERR_UNSUPPORTED;
-  const long long key_tiles = ((long long)d->S + 63) / 64 + 1;
-  if ((long long)d->B * d->Hkv >= kMaxCount / key_tiles) return LSTM_ERR_UNSUPPORTED;
+  // the backward's workgroups, of 64 rows or keys at least (the forward's are no more than its rows)
+  const long long rows = (long long)d->Tq * (d->Hq / d->Hkv), tiles = (rows + 63) / 64 + ((long long)d->S + 63) / 64;
+  if (train && (long long)d->B * d->Hkv > kMaxCount / tiles) return LSTM_ERR_UNSUPPORTED;
   return LSTM_OK;
 }
 
@@ -91,6 +92,7 @@ void plan_fwd(const lstm_attn_desc_t* d, AttnParams* p) {
   const int each = (int)((ktiles + n - 1) / n);
   p->nsplit = each > 0 ? (ktiles + each - 1) / each : 1;
   p->kv_per_split = p->nsplit > 1 ? each * kt : p->S;
+  p->blocks = (int)(blocks * p->nsplit);
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }

@@ -24,6 +24,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "dec_grid.h"
 #include "lstm_common.h"
 
 namespace lstm {
@@ -44,6 +45,7 @@ struct AttnParams {
   int rows;              // Tq * G
   int tiles;             // row tiles per (sentence, key head)
   int nsplit, kv_per_split;
+  int blocks;            // workgroups of the launch
   int kv_tiles;          // backward: key tiles per (sentence, key head)
   float scale, scale_log2;  // scale, scale * log2(e)
   float* part_o;         // nsplit > 1: [B*Hkv*rows][nsplit][D] unnormalised

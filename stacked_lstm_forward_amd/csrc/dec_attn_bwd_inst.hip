@@ -319,9 +319,10 @@ __device__ __forceinline__ void row_side(const AttnParams& p, int item, char* sm
 __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(kPerSimd)))
 attn_bwd_kernel(AttnParams p) {
   __shared__ __align__(16) char smem[kShared];
-  const int block = blockIdx.x;
-  const bool first = block < p.blocks_a;
-  const int item = first ? xcd_item(block, p.blocks_a) : xcd_item(block - p.blocks_a, gridDim.x - p.blocks_a);
+  const unsigned block = grid_block();
+  if (block >= (unsigned)p.blocks) return;
+  const bool first = block < (unsigned)p.blocks_a;
+  const int item = first ? xcd_item(block, p.blocks_a) : xcd_item(block - p.blocks_a, p.blocks - p.blocks_a);
   if (first != (p.rows_first != 0))
     key_side(p, item, smem);
   else
@@ -350,8 +351,8 @@ hipError_t DEC_FN(DEC_BF16, DEC_DP)(const AttnParams& p0, hipStream_t s) {
   // short workgroups (4 x 2048 rows, 3001 keys, D 128: 463 us, first 505).
   p.rows_first = 3ll * p.S > 8ll * p.rows;
   p.blocks_a = p.B * p.Hkv * (p.rows_first ? p.tiles : p.kv_tiles);
-  const long long n = (long long)p.B * p.Hkv * ((long long)p.tiles + p.kv_tiles);
-  hipLaunchKernelGGL(attn_bwd_kernel, dim3((unsigned)n), dim3(NT), 0, s, p);
+  p.blocks = p.B * p.Hkv * (p.tiles + p.kv_tiles);
+  hipLaunchKernelGGL(attn_bwd_kernel, grid_of(p.blocks), dim3(NT), 0, s, p);
   return hipGetLastError();
 }
 

@@ -114,7 +114,9 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
   __shared__ __align__(16) float sbiasb[2][KT];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int item = xcd_item(blockIdx.x, gridDim.x);
+  const unsigned block = grid_block();
+  if (block >= (unsigned)p.blocks) return;
+  const int item = xcd_item(block, p.blocks);
   const int tile = item % p.tiles, rest = item / p.tiles;
   const int split = rest % p.nsplit, pair = rest / p.nsplit;
   const int b = pair % p.B, hk = pair / p.B, bh = b * p.Hkv + hk;
@@ -236,7 +238,9 @@ __global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
   __shared__ float sm[NW][QC * 16], sl[NW][QC * 16];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l15 = lane & 15;
-  const int item = xcd_item(blockIdx.x, gridDim.x);
+  const unsigned block = grid_block();
+  if (block >= (unsigned)p.blocks) return;
+  const int item = xcd_item(block, p.blocks);
   const int tile = item % p.tiles, rest = item / p.tiles;
   const int split = rest % p.nsplit, pair = rest / p.nsplit;
   const int b = pair % p.B, hk = pair / p.B, bh = b * p.Hkv + hk;
@@ -376,15 +380,13 @@ __global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
 
 template <int QC, int NW, int KT>
 hipError_t launch(const AttnParams& p, hipStream_t s) {
-  const long long n = (long long)p.B * p.Hkv * p.tiles * p.nsplit;
-  hipLaunchKernelGGL((attn_fwd_kernel<ET, DP, QC, NW, KT>), dim3((unsigned)n), dim3(NW * 64), 0, s, p);
+  hipLaunchKernelGGL((attn_fwd_kernel<ET, DP, QC, NW, KT>), grid_of(p.blocks), dim3(NW * 64), 0, s, p);
   return hipGetLastError();
 }
 
 template <int QC, int NW, int KT>
 hipError_t launch_step(const AttnParams& p, hipStream_t s) {
-  const long long n = (long long)p.B * p.Hkv * p.tiles * p.nsplit;
-  hipLaunchKernelGGL((attn_step_kernel<ET, DP, QC, NW, KT>), dim3((unsigned)n), dim3(NW * 64), 0, s, p);
+  hipLaunchKernelGGL((attn_step_kernel<ET, DP, QC, NW, KT>), grid_of(p.blocks), dim3(NW * 64), 0, s, p);
   return hipGetLastError();
 }
 

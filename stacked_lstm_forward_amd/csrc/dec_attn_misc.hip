@@ -47,7 +47,7 @@ template <typename T>
 hipError_t combine(const AttnParams& p, hipStream_t s) {
   const long long rows = (long long)p.B * p.Hkv * p.rows;
   auto go = [&](auto kernel, int lr) {
-    const long long n = (rows + 256 / lr - 1) / (256 / lr);
+    const long long n = (rows + 256 / lr - 1) / (256 / lr);  // few: a split has less than 256 row tiles
     hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(256), 0, s, p);
     return hipGetLastError();
   };
@@ -64,7 +64,7 @@ hipError_t combine(const AttnParams& p, hipStream_t s) {
 template <typename T>
 __global__ void __launch_bounds__(256) attn_stats_kernel(AttnParams p) {
   constexpr int SZ = AT<T>::SZ;
-  const long long row = (long long)blockIdx.x * 16 + threadIdx.x / 16;
+  const long long row = (long long)grid_block() * 16 + threadIdx.x / 16;
   if (row >= (long long)p.B * p.Hkv * p.rows) return;
   const int r = (int)(row % p.rows), bh = (int)(row / p.rows);
   const int b = bh / p.Hkv, t = r / p.G, h = (bh % p.Hkv) * p.G + r % p.G;
@@ -101,9 +101,9 @@ hipError_t attn_combine_launch(const AttnParams& p, bool bf16, hipStream_t s) {
 hipError_t attn_stats_launch(const AttnParams& p, bool bf16, hipStream_t s) {
   const long long n = ((long long)p.B * p.Hq * p.Tq + 15) / 16;
   if (bf16)
-    hipLaunchKernelGGL((attn_stats_kernel<uint16_t>), dim3((unsigned)n), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((attn_stats_kernel<uint16_t>), grid_of(n), dim3(256), 0, s, p);
   else
-    hipLaunchKernelGGL((attn_stats_kernel<float>), dim3((unsigned)n), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((attn_stats_kernel<float>), grid_of(n), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

@@ -22,6 +22,7 @@
 #include <cmath>
 
 #include "decoder/lstm_dec.h"  // include/ is on the include path
+#include "dec_grid.h"
 #include "lstm_common.h"
 
 namespace lstm {
@@ -597,7 +598,7 @@ __global__ void __launch_bounds__(kMaxK * 64) beam_join_kernel(BeamParams p) {
 // A wave per row of h and of c: 16384 rows of 3 and 6 KiB read and written in 23.7 us,
 // 6.4 TB/s (in the join's workgroups, each with a join of its own, 65).
 __global__ void __launch_bounds__(256) beam_states_kernel(BeamParams p) {
-  const long long BK = (long long)p.B * p.K, job = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const long long BK = (long long)p.B * p.K, job = (long long)grid_block() * 4 + (threadIdx.x >> 6);
   const int which = p.h ? (p.c ? (int)(job & 1) : 0) : 1;
   const long long at = p.h && p.c ? job >> 1 : job;
   if (at >= p.L * BK) return;
@@ -701,7 +702,7 @@ lstm_status_t lstm_beam_step(const lstm_beam_desc_t* d, const void* logits, cons
   if (hipGetLastError() != hipSuccess) return LSTM_ERR_HIP;
   if (state > kCopyBytes) {
     const long long jobs = (long long)d->L * d->B * d->K * ((h ? 1 : 0) + (c ? 1 : 0));
-    hipLaunchKernelGGL(beam_states_kernel, dim3((unsigned)((jobs + 3) / 4)), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL(beam_states_kernel, grid_of((jobs + 3) / 4), dim3(256), 0, stream, p);
     if (hipGetLastError() != hipSuccess) return LSTM_ERR_HIP;
   }
   return LSTM_OK;

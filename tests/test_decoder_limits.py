@@ -31,3 +31,12 @@ def test_the_longest_key_axis_is_split():
     # two sums of D = 8 and two statistics a part and row: more than the least workspace
     d = desc(B=1, Tq=1, S=MOST, Hq=1, Hkv=1, D=8)
     assert decoder.lstm_attn_workspace_size(d) > 200 * (8 + 2) * 4
+
+
+def test_gradients_count_their_workgroups():
+    d = desc(B=1 << 30, Tq=1, S=1, Hq=1, Hkv=1, D=8)  # a tile of rows and one of keys for each sentence: 2^31
+    assert decoder.lstm_attn_validate(d) == sl.LSTM_OK
+    assert decoder.lstm_attn_validate(d, train=True) == sl.LSTM_ERR_UNSUPPORTED
+    assert decoder.lstm_attn_bwd_workspace_size(d) == 0
+    d = desc(B=(1 << 30) - 2048, Tq=1, S=1, Hq=1, Hkv=1, D=8)
+    assert decoder.lstm_attn_validate(d, train=True) == sl.LSTM_OK
