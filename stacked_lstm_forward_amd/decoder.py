@@ -17,7 +17,8 @@ and on top of it problems that own outputs and workspaces, made once per shape:
     s = prepare_beam(logits, scores, finished, lengths, eos=2, states=(h, c));  s.step()
 
 A problem reads the tensors that it was made with, whatever they hold at the
-call; ``runner.py`` is its counterpart for the recurrent stacks.
+call (or those that its attributes were set to since: they are checked like the
+first ones).  ``runner.py`` is its counterpart for the recurrent stacks.
 """
 from __future__ import annotations
 
@@ -160,11 +161,33 @@ def _workspace(n: int, device):
     return raw[off:off + n]
 
 
+class _Problem:
+    """The kernels read a problem's tensors by address, so what replaces one is checked first."""
+
+    def _runs_on(self, device) -> None:
+        if device.type != "cuda":
+            raise ValueError(f"the problem's tensors are on {device}: the kernels run on a GPU")
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            value = self._checked(name, value)
+        object.__setattr__(self, name, value)
+
+    def _workspace_like(self, t, name: str) -> None:
+        held = self.__dict__[name]
+        if held is None:
+            raise ValueError(f"{name}: the problem was made without it")
+        if t.numel() * t.element_size() < held.numel() or t.data_ptr() % 256 or not t.is_contiguous():
+            raise ValueError(f"{name}: {held.numel()} bytes, contiguous and aligned to 256")
+        if t.device != held.device:
+            raise ValueError(f"{name}: on {t.device}, expected {held.device}")
+
+
 # ---- attention ----------------------------------------------------------------
 
 
 @dataclass
-class AttnProblem:
+class AttnProblem(_Problem):
     desc: AttnDesc
     q: object
     k: object
@@ -179,8 +202,31 @@ class AttnProblem:
     dv: object = None
     bws: object = None
 
+    def __post_init__(self):
+        self.gpu = self.q.is_cuda  # (for good: what replaces a tensor is on its device)
+
+    def _checked(self, name, t):
+        import torch
+        d, device = self.desc, self.q.device
+        if name in ("q", "k", "v", "o", "dq", "dk", "dv"):
+            held = self.__dict__[name]
+            if held is None:
+                raise ValueError(f"{name}: the problem was made without gradients")
+            _like(t, name, held.shape, held.dtype, device, dense=False)
+            setattr(d, name, _rows(t, name))
+        elif name in ("kv_len", "key_mask", "lse") and t is not None:
+            shape, dtype = {"kv_len": ((d.B,), torch.int32), "key_mask": ((d.B, d.S), torch.uint8),
+                            "lse": ((d.B, d.Hq, d.Tq), torch.float32)}[name]
+            t = _bytes(t, name) if name == "key_mask" else t
+            _like(t, name, shape, dtype, device)
+        elif name in ("ws", "bws"):
+            self._workspace_like(t, name)
+        return t
+
     def forward(self, stream=None) -> None:
         """o [B, Tq, Hq, D] and lse [B, Hq, Tq]."""
+        if not self.gpu:
+            self._runs_on(self.q.device)
         n, m, e = self.kv_len, self.key_mask, self.lse
         st = _lib().lstm_attn_fwd(self.desc, self.q.data_ptr(), self.k.data_ptr(), self.v.data_ptr(),
                                   None if n is None else n.data_ptr(), None if m is None else m.data_ptr(),
@@ -193,6 +239,7 @@ class AttnProblem:
         """dq, dk, dv from dout, a tensor like o, after a forward() of the same inputs."""
         if self.bws is None:
             raise RuntimeError("backward: prepare_attn(..., train=True)")
+        self._runs_on(self.q.device)
         _like(dout, "dout", self.o.shape, self.o.dtype, self.o.device, dense=False)
         self.desc.dout = _rows(dout, "dout")
         check(lstm_attn_bwd(self.desc, self.q, self.k, self.v, self.kv_len, self.key_mask, self.o, self.lse, dout,
@@ -255,8 +302,17 @@ def prepare_attn(q, k, v, *, kv_len=None, key_mask=None, scale: Optional[float] 
 # ---- beam search --------------------------------------------------------------
 
 
+def _beam_rows(logits) -> int:
+    """Elements from one beam's logits [B, K, V] to the next."""
+    B, K, V = logits.shape
+    row = logits.stride(1) if K > 1 else (logits.stride(0) if B > 1 else V)
+    if (V > 1 and logits.stride(2) != 1) or row < V or (B > 1 and logits.stride(0) != K * row):
+        raise ValueError(f"logits: rows of contiguous values at one stride, not strides {tuple(logits.stride())}")
+    return row
+
+
 @dataclass
-class BeamProblem:
+class BeamProblem(_Problem):
     desc: BeamDesc
     logits: object
     scores: object
@@ -271,8 +327,29 @@ class BeamProblem:
     states_out: tuple
     ws: object
 
+    def _checked(self, name, t):
+        import torch
+        d, device = self.desc, self.logits.device
+        small = {"scores": torch.float32, "lengths": torch.int32, "finished": torch.uint8, "tokens": torch.int32,
+                 "parents": torch.int32}
+        kind = name[:-4] if name.endswith("_out") else name
+        if name == "logits":
+            _like(t, name, (d.B, d.K, d.V), self.logits.dtype, device, dense=False)
+            d.logits_stride = _beam_rows(t)
+        elif kind in small:
+            t = _bytes(t, name) if kind == "finished" else t
+            _like(t, name, (d.B, d.K), small[kind], device)
+        elif kind == "states":
+            for x, what, dtype in zip(t, ("h", "c"), (self.logits.dtype, torch.float32), strict=True):
+                if x is not None:
+                    _like(x, f"{name} {what}", (d.L, d.B * d.K, d.H), dtype, device)
+        elif name == "ws":
+            self._workspace_like(t, name)
+        return t
+
     def step(self, stream=None) -> None:
         """One selection: tokens, parents, scores_out, finished_out, lengths_out [B, K], states_out."""
+        self._runs_on(self.logits.device)
         check(lstm_beam_step(self.desc, self.logits, self.scores, self.finished, self.lengths, self.tokens,
                              self.parents, self.scores_out, self.finished_out, self.lengths_out, self.states[0],
                              self.states[1], self.states_out[0], self.states_out[1], self.ws,
@@ -280,11 +357,11 @@ class BeamProblem:
               "lstm_beam_step")
 
     def advance(self) -> None:
-        """Makes the step's outputs the next step's inputs (swaps the buffers; no copy)."""
-        self.scores, self.scores_out = self.scores_out, self.scores
-        self.finished, self.finished_out = self.finished_out, self.finished
-        self.lengths, self.lengths_out = self.lengths_out, self.lengths
-        self.states, self.states_out = self.states_out, self.states
+        """Makes the step's outputs the next step's inputs.  The buffers are swapped, not copied: the next
+        step() writes over the tensors that this one read, the ones the problem was made with among them."""
+        own = self.__dict__
+        for name in ("scores", "finished", "lengths", "states"):
+            own[name], own[name + "_out"] = own[name + "_out"], own[name]
 
 
 def prepare_beam(logits, scores, finished, lengths, *, eos: int, alpha: float = 0.0,
@@ -300,9 +377,7 @@ def prepare_beam(logits, scores, finished, lengths, *, eos: int, alpha: float = 
     B, K, V = logits.shape
     dt = _dtype(logits, "logits")
     dev = logits.device
-    row = logits.stride(1) if K > 1 else (logits.stride(0) if B > 1 else V)
-    if (V > 1 and logits.stride(2) != 1) or row < V or (B > 1 and logits.stride(0) != K * row):
-        raise ValueError(f"logits: rows of contiguous values at one stride, not strides {tuple(logits.stride())}")
+    row = _beam_rows(logits)
     _like(scores, "scores", (B, K), torch.float32, dev)
     finished = _bytes(finished, "finished")
     _like(finished, "finished", (B, K), torch.uint8, dev)

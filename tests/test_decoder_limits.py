@@ -1,5 +1,6 @@
 """CPU tests of the decoder operators' limits and refusals (host checks; nothing is launched)."""
 import pytest
+import torch
 
 import stacked_lstm_forward_amd as sl
 from stacked_lstm_forward_amd import decoder
@@ -40,3 +41,90 @@ def test_gradients_count_their_workgroups():
     assert decoder.lstm_attn_bwd_workspace_size(d) == 0
     d = desc(B=(1 << 30) - 2048, Tq=1, S=1, Hq=1, Hkv=1, D=8)
     assert decoder.lstm_attn_validate(d, train=True) == sl.LSTM_OK
+
+
+# ---- problems ------------------------------------------------------------------
+
+
+def attn_problem(train=True):
+    q, k = torch.zeros(2, 3, 4, 64), torch.zeros(2, 5, 2, 64)
+    return decoder.prepare_attn(q, k, k.clone(), kv_len=torch.zeros(2, dtype=torch.int32), train=train)
+
+
+def beam_problem():
+    return decoder.prepare_beam(torch.zeros(2, 4, 50), torch.zeros(2, 4), torch.zeros(2, 4, dtype=torch.uint8),
+                                torch.zeros(2, 4, dtype=torch.int32), eos=2,
+                                states=(torch.zeros(1, 8, 8), torch.zeros(1, 8, 8)))
+
+
+def test_problems_in_host_memory_do_not_run():
+    p, s = attn_problem(), beam_problem()
+    for stream in (None, 0):
+        with pytest.raises(ValueError):
+            p.forward(stream=stream)
+        with pytest.raises(ValueError):
+            p.backward(torch.zeros(2, 3, 4, 64), stream=stream)
+        with pytest.raises(ValueError):
+            s.step(stream=stream)
+
+
+@pytest.mark.parametrize("name,value,error", [
+    ("q", torch.zeros(2, 3, 4, 32), ValueError), ("k", torch.zeros(2, 4, 2, 64), ValueError),
+    ("v", torch.zeros(2, 5, 2, 64, dtype=torch.bfloat16), TypeError),
+    ("v", torch.zeros(2, 5, 2, 65)[..., 1:], ValueError), ("o", torch.zeros(2, 3, 4, 64, device="meta"), ValueError),
+    ("dk", torch.zeros(2, 5, 64, 2).transpose(2, 3), ValueError), ("kv_len", torch.zeros(1, dtype=torch.int32), ValueError),
+    ("kv_len", torch.zeros(2, dtype=torch.int64), TypeError), ("kv_len", torch.zeros(4, dtype=torch.int32)[::2], ValueError),
+    ("key_mask", torch.zeros(2, 4, dtype=torch.bool), ValueError), ("key_mask", torch.zeros(2, 5), TypeError),
+    ("lse", torch.zeros(2, 4, 2), ValueError), ("ws", torch.zeros(8, dtype=torch.uint8), ValueError),
+    ("bws", torch.zeros(1 << 12, dtype=torch.uint8)[1:], ValueError),
+])
+def test_what_replaces_a_tensor_of_an_attention_problem_is_checked(name, value, error):
+    p = attn_problem()
+    before = getattr(p, name)
+    with pytest.raises(error):
+        setattr(p, name, value)
+    assert getattr(p, name) is before
+
+
+def test_tensors_of_an_attention_problem_may_be_replaced():
+    p = attn_problem()
+    q = torch.zeros(3, 2, 4, 64).transpose(0, 1)  # another layout: its strides are the description's
+    p.q = q
+    assert p.q is q and (p.desc.q.b, p.desc.q.t, p.desc.q.h) == q.stride()[:3]
+    p.kv_len, p.lse = None, None
+    p.kv_len, p.lse = torch.ones(2, dtype=torch.int32), torch.zeros(2, 4, 3)
+    p.key_mask = torch.ones(2, 5, dtype=torch.bool)
+    assert p.key_mask.dtype == torch.uint8
+    p = attn_problem(train=False)
+    with pytest.raises(ValueError):
+        p.dq = torch.zeros(2, 3, 4, 64)
+
+
+@pytest.mark.parametrize("name,value,error", [
+    ("logits", torch.zeros(2, 4, 49), ValueError), ("logits", torch.zeros(2, 4, 50, dtype=torch.bfloat16), TypeError),
+    ("logits", torch.zeros(2, 50, 4).transpose(1, 2), ValueError), ("scores", torch.zeros(2, 3), ValueError),
+    ("scores_out", torch.zeros(2, 4, dtype=torch.float64), TypeError), ("finished", torch.zeros(2, 4), TypeError),
+    ("lengths", torch.zeros(4, 2, dtype=torch.int32).t(), ValueError), ("tokens", torch.zeros(2, 4), TypeError),
+    ("parents", torch.zeros(1, 4, dtype=torch.int32), ValueError),
+    ("states", (torch.zeros(1, 7, 8), torch.zeros(1, 8, 8)), ValueError), ("states", (torch.zeros(1, 8, 8),), ValueError),
+    ("states_out", (torch.zeros(1, 8, 8), torch.zeros(1, 8, 8, dtype=torch.bfloat16)), TypeError),
+    ("ws", torch.zeros(8, dtype=torch.uint8), ValueError),
+])
+def test_what_replaces_a_tensor_of_a_beam_problem_is_checked(name, value, error):
+    s = beam_problem()
+    before = getattr(s, name)
+    with pytest.raises(error):
+        setattr(s, name, value)
+    assert getattr(s, name) is before
+
+
+def test_tensors_of_a_beam_problem_may_be_replaced():
+    s = beam_problem()
+    s.logits = torch.zeros(2, 4, 60)[..., 3:53]
+    assert s.desc.logits_stride == 60
+    s.finished = torch.zeros(2, 4, dtype=torch.bool)
+    assert s.finished.dtype == torch.uint8
+    s.states, s.states_out = s.states_out, s.states
+    before = s.scores, s.states
+    s.advance()
+    assert s.scores_out is before[0] and s.states_out is before[1]
