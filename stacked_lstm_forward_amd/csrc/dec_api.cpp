@@ -29,6 +29,7 @@ constexpr long long kMaxCount = (1ll << 31) - 4096;
 constexpr int kComputeUnits = 256;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 // Strides are multiples of 16 bytes; outputs' elements must not coincide, which
 // is left to the caller like any other overlap.
@@ -134,6 +135,7 @@ lstm_status_t lstm_attn_fwd(const lstm_attn_desc_t* d, const void* q, const void
   const lstm_status_t st = check_desc(d, false);
   if (st != LSTM_OK) return st;
   if (!q || !o || (d->S > 0 && (!k || !v))) return LSTM_ERR_INVALID_ARG;
+  if (!aligned4(kv_len) || !aligned4(lse)) return LSTM_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return LSTM_ERR_UNSUPPORTED;
   if (!ws_ok(ws)) return LSTM_ERR_WORKSPACE;
   AttnParams p = params(d);
@@ -156,6 +158,7 @@ lstm_status_t lstm_attn_bwd(const lstm_attn_desc_t* d, const void* q, const void
   const lstm_status_t st = check_desc(d, true);
   if (st != LSTM_OK) return st;
   if (!q || !o || !lse || !dout || !dq || (d->S > 0 && (!k || !v || !dk || !dv))) return LSTM_ERR_INVALID_ARG;
+  if (!aligned4(kv_len) || !aligned4(lse)) return LSTM_ERR_INVALID_ARG;
   for (const void* x : {q, k, v, o, dout, (const void*)dq, (const void*)dk, (const void*)dv})
     if (!aligned16(x)) return LSTM_ERR_UNSUPPORTED;
   if (!ws_ok(ws)) return LSTM_ERR_WORKSPACE;

@@ -128,3 +128,18 @@ def test_tensors_of_a_beam_problem_may_be_replaced():
     before = s.scores, s.states
     s.advance()
     assert s.scores_out is before[0] and s.states_out is before[1]
+
+
+# ---- alignment -----------------------------------------------------------------
+
+
+def test_attention_refuses_lengths_and_statistics_that_are_not_aligned():
+    d = desc()
+    ok = [FAKE, FAKE, FAKE, FAKE, None, FAKE, FAKE, FAKE]
+    train = [FAKE, FAKE, FAKE, FAKE, None] + [FAKE] * 7
+    for i in (3, 6):  # kv_len, lse
+        for by in (1, 2, 3):
+            assert decoder.lstm_attn_fwd(d, *[FAKE + by if j == i else x for j, x in enumerate(ok)], stream=0) == \
+                sl.LSTM_ERR_INVALID_ARG
+            assert decoder.lstm_attn_bwd(d, *[FAKE + by if j == i else x for j, x in enumerate(train)], stream=0) == \
+                sl.LSTM_ERR_INVALID_ARG
