@@ -17,7 +17,8 @@
  * keys(b) = { s < kv_len[b] (if given) and key_mask[b][s] != 0 (if given) }.
  * A kv_len below 0 counts as 0, one above S as S.  What stands in k and v at
  * other positions is never used: infinities and NaN there change nothing.
- * Where keys(b) is empty (or S is 0), o = 0, lse = -inf and every gradient is 0.
+ * Where keys(b) is empty (or S is 0), o = 0, lse = -inf and every gradient is 0,
+ * whatever q and dout hold.
  * Gradients, with dP_s = <do, v_s> and delta = <do, o>:
  *     dv_s = sum p_s do ,  dz_s = p_s (dP_s - delta)
  *     dq = scale sum_s dz_s k_s ,  dk_s = scale sum dz_s q

@@ -312,6 +312,10 @@ __device__ __forceinline__ void row_side(const AttnParams& p, int item, char* sm
     const int r = row0 + qc * 16 + (lane & 15);
     if (r >= p.rows) continue;
     const int t = r / p.G, hq = hk * p.G + r % p.G;
+    if (nl[qc] == -INFINITY) {  // no keys: 0, whatever q and dout hold
+#pragma unroll
+      for (int n = 0; n < NTILES; ++n) dq[n][qc] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
     store_cols<ET, DP, NTILES, C>(p.dq + b * p.sdq.b + t * p.sdq.t + hq * p.sdq.h, dq, qc, p.scale, p.D, lane);
   }
 }

@@ -161,14 +161,16 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
     ck.store(skb[buf], s, s1, mb, tid, db, ck.m);
     if (tid < KT) sbiasb[buf][tid] = rb ? 0.f : -INFINITY;
   };
-  // -inf where a tile has keys left out
+  // -inf where a tile has keys left out (whatever q holds: a row without keys gives 0)
   auto leave_out = [&](f32x4 (&x)[KT / 16][QC], int s, int buf) {
     if (mb || s + KT > s1) {
 #pragma unroll
       for (int kt = 0; kt < KT / 16; ++kt) {
         const f32x4 bias = *reinterpret_cast<const f32x4*>(sbiasb[buf] + kt * 16 + (lane >> 4) * 4);
 #pragma unroll
-        for (int qc = 0; qc < QC; ++qc) x[kt][qc] += bias;
+        for (int qc = 0; qc < QC; ++qc)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[kt][qc][i] = bias[i] == 0.f ? x[kt][qc][i] : -INFINITY;
       }
     }
   };
@@ -301,17 +303,21 @@ __global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
     const uint32_t bits = mb ? (uint32_t)__ballot(mask != 0) : 0xffffffffu;
 #pragma unroll
     for (int kt = 0; kt < KT / 16; ++kt) {
-      f32x4 bias;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        bias[i] = s + kt * 16 + 4 * g + i < s1 && (bits >> (kt * 16 + 4 * g + i) & 1) ? 0.f : -INFINITY;
-#pragma unroll
-      for (int qc = 0; qc < QC; ++qc) x[kt][qc] = bias;
+      for (int qc = 0; qc < QC; ++qc) x[kt][qc] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         if (mb && !(bits >> (kt * 16 + l15) & 1)) kf[kt][c] = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int qc = 0; qc < QC; ++qc) mma_chunk<T>(x[kt][qc], kf[kt][c], qf[qc][c]);
+      }
+      // -inf for keys left out, whatever q holds: a row without keys gives 0
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = kt * 16 + 4 * g + i;
+        const bool key = s + at < s1 && (bits >> at & 1);
+#pragma unroll
+        for (int qc = 0; qc < QC; ++qc) x[kt][qc][i] = key ? x[kt][qc][i] : -INFINITY;
       }
     }
     if (s + NW * KT < s1) load_k(s + NW * KT);
