@@ -38,8 +38,8 @@
  *
  * Limits: D a multiple of 8, 8 ... 256; Hq a multiple of Hkv; q, k, v, o, dout
  * and the gradients aligned to 16 bytes and every stride a multiple of 16 bytes,
- * kv_len and lse aligned to 4; scale > 0 (0
- * selects 1/sqrt(D)); B*Hq*Tq and B*S at most 2^31 - 4096, for the gradients also
+ * kv_len and lse aligned to 4; scale > 0 and at most 2.3e38 (0 selects
+ * 1/sqrt(D)); B*Hq*Tq and B*S at most 2^31 - 4096, for the gradients also
  * B*Hkv*(ceil(Tq*Hq/(64*Hkv)) + ceil(S/64)).  Byte offsets are 64-bit.
  *
  * ---- beam search ----------------------------------------------------------

@@ -43,7 +43,7 @@ lstm_status_t check_desc(const lstm_attn_desc_t* d, bool train) {
   if (d->B < 1 || d->Tq < 1 || d->S < 0 || d->Hq < 1 || d->Hkv < 1 || d->D < 1) return LSTM_ERR_INVALID_ARG;
   if (d->dtype != LSTM_F32 && d->dtype != LSTM_BF16) return LSTM_ERR_INVALID_ARG;
   if (d->Hq % d->Hkv != 0) return LSTM_ERR_INVALID_ARG;
-  if (!(d->scale >= 0.f) || std::isinf(d->scale)) return LSTM_ERR_INVALID_ARG;
+  if (!(d->scale >= 0.f) || std::isinf(d->scale * kLog2e)) return LSTM_ERR_INVALID_ARG;  // the kernels' factor
   const int size = d->dtype == LSTM_BF16 ? 2 : 4;
   if (!stride_ok(d->q, size) || !stride_ok(d->k, size) || !stride_ok(d->v, size) || !stride_ok(d->o, size))
     return LSTM_ERR_UNSUPPORTED;

@@ -256,8 +256,8 @@ def attn_desc(q, k, v, scale: Optional[float] = None) -> AttnDesc:
     dt = _dtype(q, "q")
     _like(k, "k", (B, S, Hkv, D), q.dtype, q.device, dense=False)
     _like(v, "v", (B, S, Hkv, D), q.dtype, q.device, dense=False)
-    if scale is not None and not scale > 0:
-        raise ValueError(f"scale: {scale}, must be positive")
+    if scale is not None and not ctypes.c_float(scale).value > 0:  # (0 would select the default)
+        raise ValueError(f"scale: {scale}, must be positive in fp32")
     return AttnDesc(B, Tq, S, Hq, Hkv, D, dt, 0.0 if scale is None else scale, _rows(q, "q"), _rows(k, "k"),
                     _rows(v, "v"))
 

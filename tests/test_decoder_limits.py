@@ -143,3 +143,18 @@ def test_attention_refuses_lengths_and_statistics_that_are_not_aligned():
                 sl.LSTM_ERR_INVALID_ARG
             assert decoder.lstm_attn_bwd(d, *[FAKE + by if j == i else x for j, x in enumerate(train)], stream=0) == \
                 sl.LSTM_ERR_INVALID_ARG
+
+
+# ---- scale ---------------------------------------------------------------------
+
+
+def test_scales_that_fp32_does_not_hold_are_refused():
+    # times log2(e) they are infinite, and a score of 0 would be NaN
+    for scale in (2.4e38, 3.4e38):
+        assert decoder.lstm_attn_validate(desc(scale=scale)) == sl.LSTM_ERR_INVALID_ARG
+    assert decoder.lstm_attn_validate(desc(scale=2.3e38)) == sl.LSTM_OK
+    q, k = torch.zeros(2, 3, 4, 64), torch.zeros(2, 5, 2, 64)
+    with pytest.raises(ValueError):
+        decoder.prepare_attn(q, k, k, scale=1e-60)  # 0 in fp32, which selects 1/sqrt(D)
+    with pytest.raises(sl.LstmError):
+        decoder.prepare_attn(q, k, k, scale=1e60)
