@@ -407,7 +407,8 @@ hipError_t DEC_FN(DEC_BF16, DEC_DP)(const AttnParams& p, hipStream_t s) {
     case 0:
       if constexpr (step_max_columns(BF, DP) == 2)
         if (step_columns(BF, DP, p.rows) == 2) return launch_step<2, 4, step_key_tile(BF)>(p, s);
-      if (step_waves(BF, DP, p.rows, p.S) == 8) return launch_step<1, 8, step_key_tile(BF)>(p, s);
+      if constexpr (step_max_waves(DP) == 8)
+        if (step_waves(BF, DP, p.rows, p.S) == 8) return launch_step<1, 8, step_key_tile(BF)>(p, s);
       return launch_step<1, 4, step_key_tile(BF)>(p, s);
     case 4: return launch<QC, 4, KT>(p, s);
     default:

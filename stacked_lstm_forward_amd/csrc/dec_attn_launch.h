@@ -44,10 +44,18 @@ constexpr int step_columns(bool bf16, int dp, int rows) { return rows <= 16 ? 1 
 constexpr int fwd_rows_per_block(bool bf16, int dp, int rows) {
   return rows <= 32 ? 16 * step_columns(bf16, dp, rows) : fwd_waves(bf16, dp, rows) * 16 * fwd_columns(bf16);
 }
-// waves of the few-rows kernel: eight where four would not take all keys at once
+// Waves of the few-rows kernel: eight where four would not take all keys at once and
+// a wave's operands, sums and loads ahead fit the 256 registers that eight leave it.
+// Above a head size of 160 they spill to memory in the loop over the keys (bf16 at 192,
+// 224, 256: 12, 69, 66 registers; fp32: 28, 90, 114).  One row, 41880 keys, 16 heads, no
+// mask, eight waves and four, us: bf16 at 96 57 and 53, 128 77 and 78, 160 91 and 89, 192
+// 116 and 106, 224 220 and 119, 256 179 and 130; fp32 at 64 72 and 83, 128 134 and 135,
+// 160 164 and 166, 192 267 and 191, 224 566 and 226, 256 311 and 255.  32 x 5 rows, 1000
+// keys, 8 heads of 64: bf16 14.2 and 13.8 with a mask, fp32 23.8 and 25.6.
 constexpr int step_key_tile(bool bf16) { return bf16 ? 32 : 16; }
+constexpr int step_max_waves(int dp) { return dp <= 160 ? 8 : 4; }
 constexpr int step_waves(bool bf16, int dp, int rows, int S) {
-  return step_columns(bf16, dp, rows) == 1 && S > 4 * step_key_tile(bf16) ? 8 : 4;
+  return step_columns(bf16, dp, rows) == 1 && S > 4 * step_key_tile(bf16) ? step_max_waves(dp) : 4;
 }
 // keys that a workgroup takes together
 constexpr int fwd_keys_per_block(bool bf16, int dp, int rows, int S) {

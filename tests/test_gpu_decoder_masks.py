@@ -39,7 +39,7 @@ def test_rows_without_keys_whatever_q_and_dout_hold(shape, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows", [(1, 3), (10, 2)], ids=["one group of rows", "two groups"])
-@pytest.mark.parametrize("S", [50, 700], ids=["four waves", "eight waves"])
+@pytest.mark.parametrize("S", [50, 700], ids=["few keys", "many keys"])
 @pytest.mark.parametrize("D", [24, 96, 128, 152, 160, 192, 200, 224, 248])
 def test_few_rows(D, S, rows, dtype):
     Tq, G = rows
