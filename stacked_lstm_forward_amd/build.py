@@ -29,7 +29,7 @@ UNITS = [("lstm_kernels.hip", [])] + [
     # the decoder's attention: one unit per direction, element type and padded head size
     (f"dec_attn_{kind}_inst.hip", [f"-DDEC_BF16={bf}", f"-DDEC_DP={dp}"])
     for kind in ("fwd", "bwd") for bf in (0, 1) for dp in (256, 224, 192, 160, 128, 96, 64, 32)] + [
-    ("dec_attn_bwd_inst.hip", ["-DDEC_BF16=1", f"-DDEC_DP={dp}", "-DDEC_NARROW=1"]) for dp in (128, 96, 64, 32)] + [
+    ("dec_attn_bwd_inst.hip", ["-DDEC_BF16=1", f"-DDEC_DP={dp}", "-DDEC_NARROW=1"]) for dp in (64, 32)] + [
     ("dec_attn_misc.hip", []), ("dec_api.cpp", []), ("dec_beam.hip", [])]
 PEAK_UNITS = [("lstm_peaks.hip", [])]
 BUILD_DIR = os.path.join(HERE, "_build")

@@ -20,8 +20,7 @@ typedef hipError_t (*AttnLaunch)(const AttnParams&, hipStream_t);
 const AttnLaunch kFwd[2][8] = {DEC_ROW(fwd, 0), DEC_ROW(fwd, 1)};
 const AttnLaunch kBwd[2][8] = {DEC_ROW(bwd, 0), DEC_ROW(bwd, 1)};
 #undef DEC_ROW
-const AttnLaunch kBwdNarrow[4] = {attn_bwd_narrow_launch_1_32, attn_bwd_narrow_launch_1_64,
-                                  attn_bwd_narrow_launch_1_96, attn_bwd_narrow_launch_1_128};
+const AttnLaunch kBwdNarrow[2] = {attn_bwd_narrow_launch_1_32, attn_bwd_narrow_launch_1_64};
 
 // Lengths and row counts are held in 32 bits, and the kernels' counters step past
 // them by less than 4096 (two tiles of all waves).

@@ -31,7 +31,7 @@ typedef float ET;
 constexpr int DP = DEC_DP;
 
 #if DEC_NARROW
-constexpr int C = 1, NW = 4, RT = 32, KT = 32, kPerSimd = bwd_narrow_waves_per_simd(DEC_DP);
+constexpr int C = 1, NW = 4, RT = 32, KT = 32, kPerSimd = kBwdNarrowWavesPerSimd;
 constexpr bool kShort = false;
 #else
 constexpr int C = bwd_columns(DEC_BF16, DEC_DP), NW = bwd_waves(DEC_BF16, DEC_DP);

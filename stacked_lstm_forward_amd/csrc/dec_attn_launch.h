@@ -22,8 +22,6 @@ DEC_ATTN_DECLARE(256)
 #undef DEC_ATTN_DECLARE
 hipError_t attn_bwd_narrow_launch_1_32(const AttnParams&, hipStream_t);
 hipError_t attn_bwd_narrow_launch_1_64(const AttnParams&, hipStream_t);
-hipError_t attn_bwd_narrow_launch_1_96(const AttnParams&, hipStream_t);
-hipError_t attn_bwd_narrow_launch_1_128(const AttnParams&, hipStream_t);
 
 hipError_t attn_combine_launch(const AttnParams&, bool bf16, hipStream_t);
 hipError_t attn_stats_launch(const AttnParams&, bool bf16, hipStream_t);
@@ -61,26 +59,40 @@ constexpr int step_waves(bool bf16, int dp, int rows, int S) {
 constexpr int fwd_keys_per_block(bool bf16, int dp, int rows, int S) {
   return rows <= 32 ? step_waves(bf16, dp, rows, S) * step_key_tile(bf16) : fwd_key_tile(bf16, dp);
 }
-// 16-column groups of a backward wave: two where operands and sums of that many fit the registers
-constexpr int bwd_columns(bool bf16, int dp) { return bf16 && dp <= 128 ? 2 : 1; }
-// registers that these take on the key side
-constexpr int bwd_registers(bool bf16, int dp) { return bwd_columns(bf16, dp) * dp * (bf16 ? 12 : 16) / 16; }
-// bf16 keeps two waves a SIMD: where a wave's registers are short (192 of 256
-// here), v's operands lie in LDS, in workgroups of eight waves; elsewhere four
-// waves, whose barriers hold up fewer (D 80, 32 x 200 rows over 777 keys: 78 us, 86
-// with eight).
-constexpr bool bwd_short(bool bf16, int dp) { return bf16 && bwd_registers(bf16, dp) >= 192; }
-constexpr int bwd_waves(bool bf16, int dp) { return bwd_short(bf16, dp) ? 8 : 4; }
-constexpr int bwd_waves_per_simd(bool bf16, int dp) { return bf16 || bwd_registers(bf16, dp) < 192 ? 2 : 1; }
-// One group where there are few rows and keys: more, smaller workgroups then hide
-// each other's latency (300 rows, 400 keys at most, 192 heads of 64: 47 us, 55 with
-// two; 40 and 50, 256 heads of 128: 13 and 19; 200 and 777, 128 heads of 80: 78 and
-// 72; 1000 and 1000, 64 heads of 64: 99 and 86).
+// 16-column groups of a backward wave, bf16: two for heads of 64 at most; beyond that
+// their operands, sums and two-part products spill 32 registers and more.  us with one
+// and with two groups, 48 heads (sentences' heads) of 2048 rows and up to 3001 keys: 286
+// and 257 at 24, 372 and 335 at 64, 424 both at 96, 549 and 583 at 128; 128 heads of 100
+// rows and 3000 keys: 94 and 76, 91 and 84, 131 and 154, 172 and 225; 3000 rows and 100
+// keys: 118 and 122, 145 and 146, 223 and 257, 264 and 250.
+constexpr int bwd_columns(bool bf16, int dp) { return bf16 && dp <= 64 ? 2 : 1; }
+// For these, one group too where there are few rows and keys: more, smaller workgroups
+// then hide each other's latency.  us with one and with two groups, heads of 64: 768 of
+// 120 rows and 130 keys 45 and 61, 192 of 300 and 400 48 and 59; 128 of 600 and 600 73
+// and 75 (heads of 32: 58 both), 64 of 1000 and 1000 90 and 94 (69 and 65).
 constexpr bool bwd_narrow(bool bf16, int dp, int rows, int S) {
   return bwd_columns(bf16, dp) == 2 && rows <= 512 && S <= 512;
 }
-constexpr int bwd_narrow_waves_per_simd(int dp) { return dp <= 64 ? 4 : 3; }
+constexpr int kBwdNarrowWavesPerSimd = 4;
+// registers that operands and sums take on the key side
+constexpr int bwd_registers(bool bf16, int dp) { return bwd_columns(bf16, dp) * dp * (bf16 ? 12 : 16) / 16; }
+// bf16 runs two waves a SIMD at least (three at 96 and 128).  At 256, where the operands
+// and sums of a wave take 192 of the 256 registers that this leaves it, v's operands lie
+// in LDS, in workgroups of eight waves.  At 224 the loop spills 27 registers; with v's
+// operands in LDS it does not, which is faster for long rows and slower for short ones
+// (32 heads of 1000 rows and keys: 179 us, now 199; 256 heads of 120 and 130: 77, now 65).
+constexpr bool bwd_short(bool bf16, int dp) { return bf16 && bwd_registers(bf16, dp) >= 192; }
+constexpr int bwd_waves(bool bf16, int dp) { return bwd_short(bf16, dp) ? 8 : 4; }
+// fp32 takes one wave a SIMD from a head size of 192 on (at 256 with 29 registers spilled;
+// row and key tiles of 16 instead of 32 avoid that: 32 heads of 1000 rows and keys 1209 us,
+// now 1199, 64 heads of 100 rows and 1500 keys 395, now 438).
+constexpr int bwd_waves_per_simd(bool bf16, int dp) {
+  return bf16 ? (dp > 64 && dp <= 128 ? 3 : 2) : bwd_registers(bf16, dp) < 192 ? 2 : 1;
+}
+// Tiles of 64 where they leave LDS to the workgroups that the registers allow (at 160
+// with key tiles of 64 one workgroup of four waves fits: 269 us, now 147, for 32 heads
+// of 1000 rows and keys).
 constexpr int bwd_row_tile(bool bf16, int dp) { return bf16 && dp <= 64 ? 64 : 32; }
-constexpr int bwd_key_tile(bool bf16, int dp) { return bf16 && dp <= 160 ? 64 : 32; }
+constexpr int bwd_key_tile(bool bf16, int dp) { return bf16 && dp <= 64 ? 64 : 32; }
 
 }  // namespace lstm
