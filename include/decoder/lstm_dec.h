@@ -31,10 +31,11 @@
  * The gradients have strides of their own.  lse [B][Hq][Tq] fp32, dense.
  * kv_len [B] int32, key_mask [B][S] bytes, dense.  Products take dtype operands
  * (bf16: p and dz enter theirs as the sum of two bf16 values, within 2^-16) and
- * accumulate in fp32; softmax statistics, lse and delta are fp32 (delta is taken
- * from the o that is handed in, rounded as it is).  An infinity in v at a key or in
- * dout reaches o and the gradients as an infinity or NaN.  All sums are taken in a
- * fixed order, so results are deterministic.
+ * accumulate in fp32; softmax statistics, lse and delta are fp32.  delta is taken
+ * from the o that is handed in and, for bf16, from what o's rounding left where
+ * o_rest is given: the forward writes it there, the backward reads it.  An infinity
+ * in v at a key or in dout reaches o and the gradients as an infinity or NaN.  All
+ * sums are taken in a fixed order, so results are deterministic.
  *
  * Limits: D a multiple of 8, 8 ... 256; Hq a multiple of Hkv; q, k, v, o, dout
  * and the gradients aligned to 16 bytes and every stride a multiple of 16 bytes,
@@ -99,6 +100,8 @@ typedef struct {
   float scale;                  /* 0: 1/sqrt(D) */
   lstm_attn_stride_t q, k, v, o;
   lstm_attn_stride_t dout, dq, dk, dv; /* lstm_attn_bwd only */
+  void *o_rest;                 /* NULL, or B*Tq*Hq*D bf16 values on the device, aligned to 16 bytes: what o's
+                                   rounding leaves (training; not used for fp32) */
 } lstm_attn_desc_t;
 
 /* Checks of a description without a call (host only): the status that

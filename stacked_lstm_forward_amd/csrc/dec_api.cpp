@@ -70,6 +70,7 @@ AttnParams params(const lstm_attn_desc_t* d) {
   p.scale_log2 = p.scale * kLog2e;
   p.sq = bytes(d->q, size), p.sk = bytes(d->k, size), p.sv = bytes(d->v, size), p.so = bytes(d->o, size);
   p.sdo = bytes(d->dout, size), p.sdq = bytes(d->dq, size), p.sdk = bytes(d->dk, size), p.sdv = bytes(d->dv, size);
+  p.o_rest = size == 2 ? (char*)d->o_rest : nullptr;
   p.nsplit = 1;
   p.kv_per_split = p.S;
   return p;
@@ -135,6 +136,7 @@ lstm_status_t lstm_attn_fwd(const lstm_attn_desc_t* d, const void* q, const void
   if (st != LSTM_OK) return st;
   if (!q || !o || (d->S > 0 && (!k || !v))) return LSTM_ERR_INVALID_ARG;
   if (!aligned4(kv_len) || !aligned4(lse)) return LSTM_ERR_INVALID_ARG;
+  if (!aligned16(d->o_rest)) return LSTM_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return LSTM_ERR_UNSUPPORTED;
   if (!ws_ok(ws)) return LSTM_ERR_WORKSPACE;
   AttnParams p = params(d);
@@ -158,7 +160,7 @@ lstm_status_t lstm_attn_bwd(const lstm_attn_desc_t* d, const void* q, const void
   if (st != LSTM_OK) return st;
   if (!q || !o || !lse || !dout || !dq || (d->S > 0 && (!k || !v || !dk || !dv))) return LSTM_ERR_INVALID_ARG;
   if (!aligned4(kv_len) || !aligned4(lse)) return LSTM_ERR_INVALID_ARG;
-  for (const void* x : {q, k, v, o, dout, (const void*)dq, (const void*)dk, (const void*)dv})
+  for (const void* x : {q, k, v, o, dout, (const void*)dq, (const void*)dk, (const void*)dv, (const void*)d->o_rest})
     if (!aligned16(x)) return LSTM_ERR_UNSUPPORTED;
   if (!ws_ok(ws)) return LSTM_ERR_WORKSPACE;
   AttnParams p = params(d);

@@ -36,6 +36,7 @@ struct AttnStride {
 struct AttnParams {
   const char *q, *k, *v, *o_in, *dout;
   char *o, *dq, *dk, *dv;
+  char* o_rest;          // bf16: what o's rounding leaves, [B*Hkv][rows][D]; may be null
   float* lse;            // [B][Hq][Tq]; the forward's may be null
   const float* lse_in;   // the backward's
   const int32_t* kv_len;
@@ -216,12 +217,12 @@ __device__ __forceinline__ uint32_t rest_bf16(float x, float y, uint32_t u) {
 // rounding and the rounding of what that leaves (together within 2^-16 of p), and
 // each takes a product of its own.  One rounding of p (2^-8) would add an error as
 // large as the outputs' own rounding: 2-norm errors of o, dq, dk, dv against 64 bits
-// 0.0023, 0.0024-0.0025, 0.0024, 0.0023 instead of 0.0017, 0.0017-0.0018, 0.0017,
-// 0.0017 (fp32 products and a last rounding: 0.0017).  The second product costs
-// nothing where reading k and v is the bound (16 x 8 rows, 32768 keys: 384 us either
-// way), 15 % where latency is (64 x 200 rows, 331 keys: 16.3 and 19.0 us) and 25 to
-// 29 % of the longest cases (8 x 2048 rows, 4096 keys, 32 heads of 128: 1.22 and 1.54
-// ms; its training step with 4 x 2048 rows, 3001 keys, 12 heads: 599 and 771 us).
+// 0.0023, 0.0024-0.0025, 0.0024, 0.0023 instead of the 0.0017 that the outputs'
+// rounding alone gives.  The second product costs nothing where reading k and v is the
+// bound (16 x 8 rows, 32768 keys: 384 us either way), 15 % where latency is (64 x 200
+// rows, 331 keys: 16.3 and 19.2 us) and 25 % of the longest cases (8 x 2048 rows, 4096
+// keys, 32 heads of 128: 1.22 and 1.52 ms; the training step of 4 x 2048 rows, 3001
+// keys, 12 heads of 128: 599 and 737 us).
 template <typename T, int DP, int QC, int KT, int NTILES>
 __device__ __forceinline__ void mma_tr(f32x4 (&acc)[NTILES][QC], const char* tile, const f32x4 (&p)[KT / 16][QC],
                                        int lane) {
@@ -265,10 +266,11 @@ __device__ __forceinline__ void mma_rows(f32x4 (&s)[KT / 16][QC], const char* ti
 }
 
 // Writes one column's results (d values of lane group g) of an accumulator laid
-// out by mma_tr to a row of D values, scaled, as T.
+// out by mma_tr to a row of D values, scaled, as T; what a rounding leaves to `rest`
+// where that is given.
 template <typename T, int DP, int NTILES, int QC>
 __device__ __forceinline__ void store_cols(char* row, const f32x4 (&acc)[NTILES][QC], int qc, float by, int D,
-                                           int lane) {
+                                           int lane, char* rest = nullptr) {
   constexpr int W = TrA<T, DP>::W;
   const int g = lane >> 4;
   if constexpr (AT<T>::BF) {
@@ -276,9 +278,11 @@ __device__ __forceinline__ void store_cols(char* row, const f32x4 (&acc)[NTILES]
     for (int n = 0; n < NTILES; ++n) {
       const int d = n * 16 + 4 * g;
       if (d < D) {
-        const f32x4 x = acc[n][qc];
-        *reinterpret_cast<uint2*>(row + d * 2) =
-            make_uint2(pack_bf16(x[0] * by, x[1] * by), pack_bf16(x[2] * by, x[3] * by));
+        const f32x4 x = acc[n][qc] * by;
+        const uint2 u = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        *reinterpret_cast<uint2*>(row + d * 2) = u;
+        if (rest)
+          *reinterpret_cast<uint2*>(rest + d * 2) = make_uint2(rest_bf16(x[0], x[1], u.x), rest_bf16(x[2], x[3], u.y));
       }
     }
   } else {

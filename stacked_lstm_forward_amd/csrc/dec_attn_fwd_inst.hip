@@ -88,8 +88,9 @@ __device__ __forceinline__ void store_rows(const AttnParams& p, int b, int hk, i
     return;
   }
   const int t = r / p.G, hq = hk * p.G + r % p.G;
+  char* rest = p.o_rest ? p.o_rest + ((long long)bh * p.rows + r) * p.D * 2 : nullptr;
   store_cols<T, DP, NTILES, QC>(p.o + b * p.so.b + t * p.so.t + hq * p.so.h, o, qc, l == 0.f ? 0.f : 1.f / l, p.D,
-                                lane);
+                                lane, rest);
   if (lane < 16 && p.lse)
     p.lse[((long long)b * p.Hq + hq) * p.Tq + t] = (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
 }
@@ -375,10 +376,15 @@ __global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
       const int t = row / p.G, hq = hk * p.G + row % p.G;
       x *= lt == 0.f ? 0.f : 1.f / lt;
       char* to = p.o + b * p.so.b + t * p.so.t + hq * p.so.h + d * SZ;
-      if constexpr (AT<T>::BF)
-        *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-      else
+      if constexpr (AT<T>::BF) {
+        const uint2 u = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        *reinterpret_cast<uint2*>(to) = u;
+        if (p.o_rest)
+          *reinterpret_cast<uint2*>(p.o_rest + (((long long)bh * p.rows + row) * p.D + d) * 2) =
+              make_uint2(rest_bf16(x[0], x[1], u.x), rest_bf16(x[2], x[3], u.y));
+      } else {
         *reinterpret_cast<f32x4*>(to) = x;
+      }
       if (d == 0 && p.lse) p.lse[((long long)b * p.Hq + hq) * p.Tq + t] = mu * kLn2 + logf(lt);
     }
   }

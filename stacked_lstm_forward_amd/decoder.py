@@ -38,7 +38,8 @@ class AttnStride(ctypes.Structure):
 
 class AttnDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "Tq", "S", "Hq", "Hkv", "D", "dtype")] + [
-        ("scale", ctypes.c_float)] + [(n, AttnStride) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")]
+        ("scale", ctypes.c_float)] + [(n, AttnStride) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")] + [
+        ("o_rest", ctypes.c_void_p)]
 
 
 class BeamDesc(ctypes.Structure):
@@ -201,6 +202,7 @@ class AttnProblem(_Problem):
     dk: object = None
     dv: object = None
     bws: object = None
+    o_rest: object = None
 
     def __post_init__(self):
         self.gpu = self.q.is_cuda  # (for good: what replaces a tensor is on its device)
@@ -219,8 +221,14 @@ class AttnProblem(_Problem):
                             "lse": ((d.B, d.Hq, d.Tq), torch.float32)}[name]
             t = _bytes(t, name) if name == "key_mask" else t
             _like(t, name, shape, dtype, device)
+        elif name == "o_rest" and t is not None:
+            _like(t, name, self.o.shape, torch.bfloat16, device)
+            if t.dtype != self.o.dtype or t.data_ptr() % 16:
+                raise ValueError("o_rest: of bf16 problems, aligned to 16 bytes")
         elif name in ("ws", "bws"):
             self._workspace_like(t, name)
+        if name == "o_rest":
+            d.o_rest = None if t is None else t.data_ptr()
         return t
 
     def forward(self, stream=None) -> None:
@@ -296,7 +304,9 @@ def prepare_attn(q, k, v, *, kv_len=None, key_mask=None, scale: Optional[float] 
     lse = torch.empty((B, desc.Hq, desc.Tq), dtype=torch.float32, device=q.device)
     ws = _workspace(lstm_attn_workspace_size(desc), q.device)
     bws = _workspace(lstm_attn_bwd_workspace_size(desc), q.device) if train else None
-    return AttnProblem(desc, q, k, v, kv_len, key_mask, o, lse, ws, dq, dk, dv, bws)
+    rest = torch.empty(q.shape, dtype=q.dtype, device=q.device) if train and q.dtype == torch.bfloat16 else None
+    desc.o_rest = _ptr(rest)
+    return AttnProblem(desc, q, k, v, kv_len, key_mask, o, lse, ws, dq, dk, dv, bws, rest)
 
 
 # ---- beam search --------------------------------------------------------------

@@ -100,6 +100,22 @@ def test_tensors_of_an_attention_problem_may_be_replaced():
         p.dq = torch.zeros(2, 3, 4, 64)
 
 
+def test_what_the_rounding_of_o_leaves_has_a_place_of_its_own():
+    assert attn_problem().o_rest is None and not attn_problem().desc.o_rest  # fp32
+    q, k = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 5, 2, 64, dtype=torch.bfloat16)
+    assert decoder.prepare_attn(q, k, k).o_rest is None
+    p = decoder.prepare_attn(q, k, k, train=True)
+    assert p.o_rest.numel() == p.o.numel() and p.desc.o_rest == p.o_rest.data_ptr()
+    p.o_rest = None
+    assert not p.desc.o_rest
+    for bad, error in ((torch.zeros(2, 3, 4, 32, dtype=torch.bfloat16), ValueError), (torch.zeros(2, 3, 4, 64), TypeError)):
+        with pytest.raises(error):
+            p.o_rest = bad
+    d = desc(o_rest=FAKE + 8)
+    assert decoder.lstm_attn_fwd(d, *[FAKE] * 3, None, None, *[FAKE] * 3, stream=0) == sl.LSTM_ERR_UNSUPPORTED
+    assert decoder.lstm_attn_bwd(d, *[FAKE] * 3, None, None, *[FAKE] * 7, stream=0) == sl.LSTM_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("name,value,error", [
     ("logits", torch.zeros(2, 4, 49), ValueError), ("logits", torch.zeros(2, 4, 50, dtype=torch.bfloat16), TypeError),
     ("logits", torch.zeros(2, 50, 4).transpose(1, 2), ValueError), ("scores", torch.zeros(2, 3), ValueError),

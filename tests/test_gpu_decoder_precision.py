@@ -2,7 +2,7 @@
 
 Attention in bf16: p and dz enter their products with 16 bits, not 8.  Bounds, element by element: the
 output's own rounding (u = eps / 2 of the type), 2^-16 of p or dz for their two-part products, the fp32
-arithmetic (as in ``decoder_reference``), and for dq and dk the rounding of the o that delta is taken from.
+arithmetic (as in ``decoder_reference``); delta takes o with 16 bits too (o and o_rest).
 
 Beam search: the largest logits' exponentials count in 64 bits, the others' share of the sum in fp32 (all
 roundings one way, that share is off by 2^-19 of itself).
@@ -14,7 +14,7 @@ import torch
 
 from stacked_lstm_forward_amd import decoder
 
-from .decoder_reference import beam
+from .decoder_reference import attention, beam
 from .test_gpu_decoder import DEV, DT, beam_inputs, check_beam, tensors, within
 
 pytestmark = pytest.mark.gpu
@@ -47,7 +47,7 @@ def bounds(q, k, v, dout):
     o = p @ vd
     e_o = U * o.abs() + (P + rel) * (p @ vd.abs())
     delta, dp = (dd * o).sum(-1, keepdim=True), dd @ t(vd)
-    e_delta = (dd.abs() * (e_o + W * (D + 2) * o.abs())).sum(-1, keepdim=True)
+    e_delta = (dd.abs() * ((P + W * (D + 2)) * o.abs() + (P + rel) * (p @ vd.abs()))).sum(-1, keepdim=True)
     dz = p * (dp - delta)
     n = W * (G * Tq + S + 8)
     e_dz = p * (W * (D + 2) * (dd.abs() @ t(vd.abs())) + e_delta) + (P + 2 * rel + n) * dz.abs()
@@ -60,7 +60,8 @@ def bounds(q, k, v, dout):
 
 @pytest.mark.parametrize("shape", [(2, 300, 700, 4, 2, 64), (1, 600, 530, 2, 2, 128), (2, 200, 300, 2, 1, 80),
                                    (1, 150, 900, 2, 2, 200), (2, 5, 400, 4, 2, 128), (3, 1, 900, 4, 4, 64),
-                                   (1, 24, 333, 2, 2, 96)], ids=str)
+                                   (1, 24, 333, 2, 2, 96), (2, 300, 10, 2, 1, 64), (4, 50, 3, 2, 2, 128),
+                                   (1, 40, 5000, 1, 1, 64), (2, 600, 2, 1, 1, 32)], ids=str)
 def test_products_hold_p_and_dz_in_sixteen_bits(shape):
     q, k, v, do = tensors(*shape, "bf16", seed=21)
     p = decoder.prepare_attn(q, k, v, train=True)
@@ -68,6 +69,15 @@ def test_products_hold_p_and_dz_in_sixteen_bits(shape):
     p.backward(do)
     for name, want in bounds(q, k, v, do).items():
         within(getattr(p, name), want, name)
+    p.o_rest = None  # without it delta is taken from the rounded o, and o is the same
+    o = p.o.clone()
+    p.o.zero_()
+    p.forward()
+    p.backward(do)
+    assert torch.equal(p.o, o)
+    want = attention(q, k, v, None, None, do)
+    for name in ("dq", "dk", "dv"):
+        within(getattr(p, name), want[name], name)
 
 
 # ---- beam search ---------------------------------------------------------------
