@@ -177,33 +177,38 @@ __device__ __forceinline__ void mma_tr_bf16(f32x4 (&acc)[NTILES][QC], const char
   }
 }
 
-template <int DP, int QC, int NTILES>
-__device__ __forceinline__ void mma_tr_f32(f32x4 (&acc)[NTILES][QC], const char* tile, const f32x4 (&p)[QC],
+// acc += (KT rows of `tile`, transposed) * p in fp32.  A tile's sum is taken by itself
+// and then added, so that a long sum takes KT roundings and one for each tile, not one
+// for each row (dv of 20000 rows: 2-norm error 2.6e-6 row by row).
+template <int DP, int QC, int KT, int NTILES>
+__device__ __forceinline__ void mma_tr_f32(f32x4 (&acc)[NTILES][QC], const char* tile, const f32x4 (&p)[KT / 16][QC],
                                            int lane) {
   constexpr int PB = Pitch<float, DP>::B;
   constexpr int W = TrA<float, DP>::W;
-  const int g = lane >> 4, m = lane & 15;
+  typedef float Wide __attribute__((ext_vector_type(W)));
+  const char* base = tile + 4 * (lane >> 4) * PB + (lane & 15) * W * 4;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const char* base = tile + (4 * g + i) * PB + m * W * 4;
+  for (int u = 0; u < NTILES / W; ++u) {
+    f32x4 sum[W][QC];
 #pragma unroll
-    for (int u = 0; u < NTILES / W; ++u) {
-      float a[W];
-      if constexpr (W == 4) {
-        const f32x4 x = *reinterpret_cast<const f32x4*>(base + u * 16 * W * 4);
+    for (int t = 0; t < W; ++t)
 #pragma unroll
-        for (int t = 0; t < W; ++t) a[t] = x[t];
-      } else {
-        const f32x2 x = *reinterpret_cast<const f32x2*>(base + u * 16 * W * 4);
+      for (int qc = 0; qc < QC; ++qc) sum[t][qc] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int t = 0; t < W; ++t) a[t] = x[t];
+    for (int kt = 0; kt < KT / 16; ++kt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Wide a = *reinterpret_cast<const Wide*>(base + (kt * 16 + i) * PB + u * 16 * W * 4);
+#pragma unroll
+        for (int t = 0; t < W; ++t)
+#pragma unroll
+          for (int qc = 0; qc < QC; ++qc)
+            sum[t][qc] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[t], p[kt][qc][i], sum[t][qc], 0, 0, 0);
       }
 #pragma unroll
-      for (int t = 0; t < W; ++t)
+    for (int t = 0; t < W; ++t)
 #pragma unroll
-        for (int qc = 0; qc < QC; ++qc)
-          acc[u * W + t][qc] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[t], p[qc][i], acc[u * W + t][qc], 0, 0, 0);
-    }
+      for (int qc = 0; qc < QC; ++qc) acc[u * W + t][qc] += sum[t][qc];
   }
 }
 
@@ -226,8 +231,8 @@ __device__ __forceinline__ uint32_t rest_bf16(float x, float y, uint32_t u) {
 template <typename T, int DP, int QC, int KT, int NTILES>
 __device__ __forceinline__ void mma_tr(f32x4 (&acc)[NTILES][QC], const char* tile, const f32x4 (&p)[KT / 16][QC],
                                        int lane) {
-  constexpr int PB = Pitch<T, DP>::B;
   if constexpr (AT<T>::BF) {
+    constexpr int PB = Pitch<T, DP>::B;
 #pragma unroll
     for (int ks = 0; ks < KT / 32; ++ks) {
       uint4 hi[QC], lo[QC];
@@ -243,8 +248,7 @@ __device__ __forceinline__ void mma_tr(f32x4 (&acc)[NTILES][QC], const char* til
       mma_tr_bf16<T, DP, QC, NTILES>(acc, tile + ks * 32 * PB, hi, lo, lane);
     }
   } else {
-#pragma unroll
-    for (int kt = 0; kt < KT / 16; ++kt) mma_tr_f32<DP, QC, NTILES>(acc, tile + kt * 16 * PB, p[kt], lane);
+    mma_tr_f32<DP, QC, KT, NTILES>(acc, tile, p, lane);
   }
 }
 

@@ -45,22 +45,25 @@ __device__ __forceinline__ void raise_max(const float (&mn)[QC], f32x4 (&o)[NTIL
   }
 }
 
-// Scores become exponentials, their sum goes to l.
+// Scores become exponentials, their sum goes to l (a tile's by itself first: a long
+// sum then takes one rounding of its own size a tile, not one a key).
 template <int QC, int KT>
 __device__ __forceinline__ void tile_exp(f32x4 (&x)[KT / 16][QC], const float (&m)[QC], float (&l)[QC],
                                          float scale_log2) {
 #pragma unroll
-  for (int kt = 0; kt < KT / 16; ++kt)
+  for (int qc = 0; qc < QC; ++qc) {
+    const float mu = m[qc] == -INFINITY ? 0.f : m[qc];
+    float sum = 0.f;
 #pragma unroll
-    for (int qc = 0; qc < QC; ++qc) {
-      const float mu = m[qc] == -INFINITY ? 0.f : m[qc];
+    for (int kt = 0; kt < KT / 16; ++kt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float e = exp2_fast(fmaf(x[kt][qc][i], scale_log2, -mu));
         x[kt][qc][i] = e;
-        l[qc] += e;
+        sum += e;
       }
-    }
+    l[qc] += sum;
+  }
 }
 
 template <typename T, int DP, int QC, int KT, int NTILES>

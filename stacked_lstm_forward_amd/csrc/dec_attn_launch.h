@@ -83,11 +83,10 @@ constexpr int bwd_registers(bool bf16, int dp) { return bwd_columns(bf16, dp) * 
 // (32 heads of 1000 rows and keys: 179 us, now 199; 256 heads of 120 and 130: 77, now 65).
 constexpr bool bwd_short(bool bf16, int dp) { return bf16 && bwd_registers(bf16, dp) >= 192; }
 constexpr int bwd_waves(bool bf16, int dp) { return bwd_short(bf16, dp) ? 8 : 4; }
-// fp32 takes one wave a SIMD from a head size of 192 on (at 256 with 29 registers spilled;
-// row and key tiles of 16 instead of 32 avoid that: 32 heads of 1000 rows and keys 1209 us,
-// now 1199, 64 heads of 100 rows and 1500 keys 395, now 438).
+// fp32 runs three up to 64 (512 heads of 100 rows and 120 keys: 73 us, 80 with two), two
+// up to 128, then one.
 constexpr int bwd_waves_per_simd(bool bf16, int dp) {
-  return bf16 ? (dp > 64 && dp <= 128 ? 3 : 2) : bwd_registers(bf16, dp) < 192 ? 2 : 1;
+  return bf16 ? (dp > 64 && dp <= 128 ? 3 : 2) : dp <= 64 ? 3 : bwd_registers(bf16, dp) < 192 ? 2 : 1;
 }
 // Tiles of 64 where they leave LDS to the workgroups that the registers allow (at 160
 // with key tiles of 64 one workgroup of four waves fits: 269 us, now 147, for 32 heads

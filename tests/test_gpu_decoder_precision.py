@@ -80,6 +80,27 @@ def test_products_hold_p_and_dz_in_sixteen_bits(shape):
         within(getattr(p, name), want[name], name)
 
 
+def test_long_fp32_sums_round_once_a_tile():
+    """32768 equal terms just above 1: added one by one, a sum of 2^14 and more loses what is above 1
+    (2e-4 of each term).  Tiles of 32 terms that are added then leave half a step each."""
+    n, term = 1 << 15, 1.0 + 7 * 2.0 ** -15
+    bound = (n / 32 + 32 + 8) * W  # a tile's own terms, the tiles, p and the last factors
+    # dv: one key, 8 heads of 4096 rows share it
+    q = torch.zeros(1, n // 8, 8, 32, device=DEV)
+    k, v = torch.zeros(1, 1, 1, 32, device=DEV), torch.ones(1, 1, 1, 32, device=DEV)
+    p = decoder.prepare_attn(q, k, v, train=True)
+    p.forward()
+    p.backward(torch.full_like(q, term))
+    assert float((p.dv.double() / (n * term) - 1).abs().max()) <= bound
+    # o: 32768 keys of equal scores, with rows enough that the key axis is not split
+    q = torch.zeros(256, 40, 1, 32, device=DEV)
+    k = torch.zeros(1, n, 1, 32, device=DEV).expand(256, n, 1, 32)
+    v = torch.full((1, n, 1, 32), term, device=DEV).expand(256, n, 1, 32)
+    p = decoder.prepare_attn(q, k, v)
+    p.forward()
+    assert float((p.o.double() / term - 1).abs().max()) <= bound
+
+
 # ---- beam search ---------------------------------------------------------------
 
 
