@@ -101,12 +101,15 @@ __device__ __forceinline__ void store_rows(const AttnParams& p, int b, int hk, i
 // Each wave owns 16*QC rows (columns of S^T), the workgroup's NW waves share
 // the KT keys of a tile in LDS, so that a byte read from there feeds QC products.
 // One pass over the keys with the running maximum and sum.  Long rows are bound by
-// the exponentials and rescaling that the matrix products only partly hide (matrix
-// pipe busy 38 % of the time, no bank conflicts): 8 x 2048 rows, 4096 keys, 32
-// heads of 128, bf16 1.21 ms = 906 TFLOP/s, where a library product of 8192^3
-// reaches 1108; one tile at a time instead of two interleaved took 1.57 ms.  Short
-// ones (64 x 200 rows, 331 keys, 4 heads of 64: 16.8 us, 5.9 for its bytes) are bound
-// by the latency of six dependent tiles.
+// matrix and vector work that two waves a SIMD overlap only partly (matrix pipe busy
+// 45 % of the time, vector pipe 48 %, no bank conflicts): 8 x 2048 rows, 4096 keys, 32
+// heads of 128, bf16 1.52 ms = 722 TFLOP/s (1084 with the second product of p), where a
+// library product of 8192^3 reaches 1108.  With p rounded once it took 1.21 ms, and
+// then one tile at a time instead of two interleaved 1.57.  Short ones (64 x 200 rows,
+// 331 keys, 4 heads of 64: 19.5 us, 5.9 for its bytes) are bound by the latency of six
+// dependent tiles, whose loads are issued one tile ahead.  Heads of 136 to 256 in bf16
+// run four waves of up to 476 registers, one a SIMD: every tile's latency shows (4 x
+// 2000 rows, 2000 keys, 8 heads of 256: 287 us, 118 for its products).
 template <typename T, int DP, int QC, int NW, int KT>
 __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
   constexpr int SZ = AT<T>::SZ, NT = NW * 64, PB = Pitch<T, DP>::B;
@@ -229,9 +232,10 @@ __global__ void __launch_bounds__(NW * 64) attn_fwd_kernel(AttnParams p) {
 // a slice of LDS that only its wave touches: no barrier until the waves' results
 // are joined, in one step.  Bound by the reading of k and v; a tile's loads are in
 // flight while its predecessor is computed.  16 x 8 rows, 32768 keys, 32/8 heads of
-// 128, bf16: 390 us = 5.5 TB/s (a copy reaches 5.0); 32 x 5 rows, 1000 keys, 8 heads
-// of 64: 11.9 us, 4.2 TB/s (with four waves, a split and a second launch 15.7); one
-// row over 100 keys: 4.8 us, a launch.
+// 128, bf16: 380 us = 5.6 TB/s (a copy reaches 5.0); 32 x 5 rows, 1000 keys, 8 heads
+// of 64: 12.5 us, 4.0 TB/s, fp32 20.8 us, 4.8 TB/s; one row over 100 keys: 4.8 us, a
+// launch.  Heads of 32 in bf16 reach half of that (6 rows of 64/8 heads, 31554 keys:
+// 75 us, 2.6 TB/s): a head's row is half a cache line.
 template <typename T, int DP, int QC, int NW, int KT>
 __global__ void __launch_bounds__(NW * 64) attn_step_kernel(AttnParams p) {
   constexpr int SZ = AT<T>::SZ, PB = Pitch<T, DP>::B;
@@ -416,7 +420,7 @@ hipError_t DEC_FN(DEC_BF16, DEC_DP)(const AttnParams& p, hipStream_t s) {
     case 0:
       if constexpr (step_max_columns(BF, DP) == 2)
         if (step_columns(BF, DP, p.rows) == 2) return launch_step<2, 4, step_key_tile(BF)>(p, s);
-      if constexpr (step_max_waves(DP) == 8)
+      if constexpr (step_max_waves(BF, DP) == 8)
         if (step_waves(BF, DP, p.rows, p.S) == 8) return launch_step<1, 8, step_key_tile(BF)>(p, s);
       return launch_step<1, 4, step_key_tile(BF)>(p, s);
     case 4: return launch<QC, 4, KT>(p, s);

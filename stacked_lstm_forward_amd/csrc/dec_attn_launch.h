@@ -30,7 +30,10 @@ hipError_t attn_stats_launch(const AttnParams&, bool bf16, hipStream_t);
 // Waves of a workgroup with rows of their own: 0 selects the kernel whose waves
 // own keys (up to 32 rows, one or two column groups).
 constexpr int fwd_columns(bool bf16) { return bf16 ? 2 : 1; }
-constexpr int fwd_key_tile(bool bf16, int dp) { return bf16 && dp <= 160 ? 64 : 32; }
+// (fp32 above 192: with tiles of 32 a wave of eight spills beside a tile's own sums; 32
+// heads of 1000 rows and keys at 224 and 256 263 and 290 us, with four waves 287 and 342,
+// spilling 323 and 376)
+constexpr int fwd_key_tile(bool bf16, int dp) { return bf16 ? (dp <= 160 ? 64 : 32) : dp > 192 ? 16 : 32; }
 // eight waves share a tile where their operands and sums fit 256 registers a lane
 constexpr int fwd_max_waves(bool bf16, int dp) { return bf16 && dp > 128 ? 4 : 8; }
 constexpr int fwd_waves(bool bf16, int dp, int rows) {
@@ -44,16 +47,16 @@ constexpr int fwd_rows_per_block(bool bf16, int dp, int rows) {
 }
 // Waves of the few-rows kernel: eight where four would not take all keys at once and
 // a wave's operands, sums and loads ahead fit the 256 registers that eight leave it.
-// Above a head size of 160 they spill to memory in the loop over the keys (bf16 at 192,
-// 224, 256: 12, 69, 66 registers; fp32: 28, 90, 114).  One row, 41880 keys, 16 heads, no
-// mask, eight waves and four, us: bf16 at 96 57 and 53, 128 77 and 78, 160 91 and 89, 192
-// 116 and 106, 224 220 and 119, 256 179 and 130; fp32 at 64 72 and 83, 128 134 and 135,
-// 160 164 and 166, 192 267 and 191, 224 566 and 226, 256 311 and 255.  32 x 5 rows, 1000
-// keys, 8 heads of 64: bf16 14.2 and 13.8 with a mask, fp32 23.8 and 25.6.
+// Above a head size of 160 (fp32 128) they spill to memory in the loop over the keys.
+// One row, 41880 keys, 16 heads, no mask, eight waves and four, us: bf16 at 96 57 and 53,
+// 128 77 and 78, 160 91 and 89, 192 116 and 106, 224 220 and 119, 256 179 and 130; fp32 at
+// 64 72 and 83, 128 134 and 135, 160 168 and 165, 192 267 and 191, 224 566 and 226, 256 311
+// and 255.  32 x 5 rows, 1000 keys, 8 heads: bf16 at 64 14.2 and 13.8 with a mask; fp32 at
+// 64 23.8 and 25.6, at 160 66 and 61.
 constexpr int step_key_tile(bool bf16) { return bf16 ? 32 : 16; }
-constexpr int step_max_waves(int dp) { return dp <= 160 ? 8 : 4; }
+constexpr int step_max_waves(bool bf16, int dp) { return dp <= (bf16 ? 160 : 128) ? 8 : 4; }
 constexpr int step_waves(bool bf16, int dp, int rows, int S) {
-  return step_columns(bf16, dp, rows) == 1 && S > 4 * step_key_tile(bf16) ? step_max_waves(dp) : 4;
+  return step_columns(bf16, dp, rows) == 1 && S > 4 * step_key_tile(bf16) ? step_max_waves(bf16, dp) : 4;
 }
 // keys that a workgroup takes together
 constexpr int fwd_keys_per_block(bool bf16, int dp, int rows, int S) {
