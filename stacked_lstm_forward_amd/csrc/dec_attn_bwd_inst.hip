@@ -9,14 +9,15 @@
 // order: no atomics, no partial dq in memory.  In one launch the tail of one kind
 // is filled by the other.
 //
-// Bound by the latency of the four dependent products of a tile at two waves a
-// SIMD, all that 256 registers a lane allow (matrix pipe busy 43 % of a working
-// compute unit's time), and by the last round of workgroups: 4 x 2048 rows, 3001
-// keys at most, 12 heads of 128, bf16 470 us, 420 TFLOP/s with the repeated
-// products (two launches, one wave a SIMD: 834).  32 x 200 rows, 777 keys, 4 key
-// heads of 80: 68 us, the fixed cost of a workgroup being about as large as its 7
-// or 13 tiles.  fp32, 64 x 100 rows, 120 keys at most, 8 heads of 64: 76 us, 43 of them
-// matrix products.
+// Bound by the latency of the dependent products of a tile at two or three waves a
+// SIMD (matrix pipe busy 44 % of a working compute unit's time, vector pipe 45 %, LDS
+// 43 %), and by the last round of workgroups: 4 x 2048 rows, 3001 keys at most, 12
+// heads of 128, bf16 536 us, 740 TFLOP/s with the repeated products (the second ones
+// of p and dz not counted).  32 x 200 rows, 777 keys, 4 key heads of 80: 80 us, the
+// fixed cost of a workgroup being about as large as its 7 or 25 tiles.  fp32, 64 x 100
+// rows, 120 keys at most, 8 heads of 64: 74 us, 55 % of it matrix products.  Where there
+// are fewer workgroups than compute units, each still walks its whole other axis: 2 x
+// 2000 rows, 200 keys, 2 heads of 64 take 72 us for 1.4 GFLOP.
 #include "dec_attn.h"
 #include "dec_attn_launch.h"
 

@@ -275,16 +275,17 @@ __device__ __forceinline__ void list_best(float* lv, int* li, int n, int K, int 
 // case the proposals of beams closer than that could change places; normal logits of
 // deviation 0.5 to 5 leave 2^-26 (1000 values) to 2^-29 (131072); where the listed
 // values hold nearly all of the sum, it is as exact as 64 bits.  All exponentials in
-// fp32, with X up to 16 below the largest value, took 122 instead of 131 us (below)
-// and left up to 2^-20.
+// fp32, with X up to 16 below the largest value, left up to 2^-20 (the step below:
+// 152 us, now 154).  The exponentials are taken before a step's list is looked at: after
+// it (154 and 167 us), or of values changed by it (205), they wait for it.
 //
-// 2048 rows of 131072 bf16 values, 85 % of them read: 131 us, 3.5 TB/s; vector
-// instructions take about 70 % of that time (eight exponentials at a quarter of the
+// 2048 rows of 131072 bf16 values, 85 % of them read: 121 us, 3.8 TB/s; vector
+// instructions take 71 % of that time (eight exponentials at a quarter of the
 // rate per vector, and the list).  320 rows of 32007: 15 us, latency: a wave has
 // nine steps, and its list to sort.  Keeping vectors instead of values in the list
-// (18.9 and 129 us), or a first bound from maxima of groups of lanes (17.3 and 131:
-// more to collect), was slower; rereading the best lanes' vectors at the end instead
-// of a list 183 and 19.
+// (18.9 and 129 us, then 15 and 124), or a first bound from maxima of groups of lanes
+// (17.3 and 131: more to collect), was slower; rereading the best lanes' vectors at the
+// end instead of a list 19 and 183.
 template <bool BF>
 __global__ void __launch_bounds__(256) beam_rows_kernel(BeamParams p) {
   constexpr int VE = Row<BF>::VE;
@@ -489,7 +490,7 @@ __device__ __forceinline__ void copy_row(const BeamParams& p, int which, long lo
   }
 }
 
-// A wave per beam.  Latency: 5.6 us for one sentence of 4 beams of 8 parts, 10 us for
+// A wave per beam.  Latency: 5.5 us for one sentence of 4 beams of 8 parts, 9 us for
 // 256 sentences of 8 beams.
 __global__ void __launch_bounds__(kMaxK * 64) beam_join_kernel(BeamParams p) {
   extern __shared__ char heads[];  // [K][parts * K] values, then indexes: a beam's parts' best
@@ -595,8 +596,8 @@ __global__ void __launch_bounds__(kMaxK * 64) beam_join_kernel(BeamParams p) {
   }
 }
 
-// A wave per row of h and of c: 16384 rows of 3 and 6 KiB read and written in 23.7 us,
-// 6.4 TB/s (in the join's workgroups, each with a join of its own, 65).
+// A wave per row of h and of c: 16384 rows of 3 or 6 KiB read and written in 23 us,
+// 6.6 TB/s (in the join's workgroups, each with a join of its own, 65).
 __global__ void __launch_bounds__(256) beam_states_kernel(BeamParams p) {
   const long long BK = (long long)p.B * p.K, job = (long long)grid_block() * 4 + (threadIdx.x >> 6);
   const int which = p.h ? (p.c ? (int)(job & 1) : 0) : 1;

@@ -277,7 +277,8 @@ def prepare_attn(q, k, v, *, kv_len=None, key_mask=None, scale: Optional[float] 
     The heads' values are contiguous, the other strides free (multiples of 16 bytes): a stack's
     [T][B][H] outputs enter as ``y.view(T, B, heads, D).transpose(0, 1)``.  kv_len [B] int32 and
     key_mask [B, S] (uint8 or bool, 0 leaves a key out) may each be given.  Outputs and gradients
-    have the layout of the tensor they belong to.
+    have the layout of the tensor they belong to.  With train, a bf16 problem also keeps what o's
+    rounding leaves (o_rest), from which backward() takes <dout, o>.
     """
     import torch
     desc = attn_desc(q, k, v, scale)
