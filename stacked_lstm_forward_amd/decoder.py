@@ -107,11 +107,14 @@ def lstm_beam_step(desc, logits, scores, finished, lengths, tokens, parents, sco
 
 def _on(stream, t) -> int:
     """The stream's handle; by default the current stream of t's device (a single token's launch is
-    short beside building a torch.cuda.Stream object, so the handle is asked for directly)."""
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(t.device.index)
-    return _stream(stream)
+    short beside building a torch.cuda.Stream object, so the handle is asked for directly).  That device
+    has to be the current one: a default stream's handle is 0 on every device, and the launch would go
+    to the current device with addresses of the other."""
+    import torch
+    index = t.device.index
+    if torch._C._cuda_getDevice() != index:
+        raise ValueError(f"the problem's tensors are on {t.device}, which is not the current device")
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
 
 
 # ---- checks of tensors (host only) --------------------------------------------

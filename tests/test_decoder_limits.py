@@ -174,3 +174,16 @@ def test_scales_that_fp32_does_not_hold_are_refused():
         decoder.prepare_attn(q, k, k, scale=1e-60)  # 0 in fp32, which selects 1/sqrt(D)
     with pytest.raises(sl.LstmError):
         decoder.prepare_attn(q, k, k, scale=1e60)
+
+
+def test_problems_run_on_the_current_device(monkeypatch):
+    class Tensor:
+        device = torch.device("cuda:1")
+
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 64 * index, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    assert decoder._on(None, Tensor) == 64 and decoder._on(7, Tensor) == 7
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    for stream in (None, 7):
+        with pytest.raises(ValueError):
+            decoder._on(stream, Tensor)
