@@ -49,21 +49,22 @@ __device__ __forceinline__ Map map_join(const Map& later, const Map& earlier) {
   return {later.A * earlier.A, map_apply(later, earlier.G)};
 }
 
-// Candidates.  For bf16 values r = 1 / (1 + exp(2|u|)), with u's sign, gives both tanh(u) = 1 - 2r and its
-// slope 4r (1 - r).  Near 0 that is off by some 2^-22, which from |u| = 2^-13 on is less than what the rounding of
-// u to bf16 itself means; the fp32 form costs twice as much (10 to 15 % of the passes' time at 32 x 500 x 4096).
+// Candidates.  For bf16 values tanh(u) = 1 - 2r with r = 1 / (1 + exp(2|u|)), and its slope 4r (1 - r).  1 - 2r
+// cancels near 0, so |u| < 2^-4 takes u - u^3/3, whose next term is 2/15 u^4 of it: either is within 2^-17.5 of
+// tanh(u), relative to it, 2^-8.5 of what the rounding of u to bf16 means.  (The fp32 form costs twice as much, 10 to
+// 15 % of the passes' time at 32 x 500 x 4096.)
 __device__ __forceinline__ float tanh_part(float u) {
-  const float t = __builtin_amdgcn_exp2f(2.88539008f * __builtin_fabsf(u));
-  return __builtin_copysignf(__builtin_amdgcn_rcpf(1.f + t), u);
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(2.88539008f * __builtin_fabsf(u)));
 }
-__device__ __forceinline__ float tanh_from(float r) { return __builtin_fmaf(-2.f, r, __builtin_copysignf(1.f, r)); }
-__device__ __forceinline__ float slope_from(float r) { return __builtin_fmaf(-4.f * r, r, 4.f * __builtin_fabsf(r)); }
 
 // For fp32 values tanh(u) = (1 - e) / (1 + e) with e = exp(-2|u|); below 1/4 its series, whose next term
 // is 0.009 u^11, since 1 - e cancels there.
 template <bool BF>
 __device__ __forceinline__ float tanh_of(float u) {
-  if constexpr (BF) return tanh_from(tanh_part(u));
+  if constexpr (BF) {
+    const float near = __builtin_fmaf(u * u, u * -0.33333333f, u);
+    return __builtin_fabsf(u) < 0.0625f ? near : __builtin_copysignf(__builtin_fmaf(-2.f, tanh_part(u), 1.f), u);
+  }
   const float e = exp_of<BF>(-2.f * __builtin_fabsf(u));
   const float far = (1.f - e) * __builtin_amdgcn_rcpf(1.f + e);
   const float v = u * u;
@@ -75,7 +76,12 @@ __device__ __forceinline__ float tanh_of(float u) {
 }
 
 // 1 - tanh(u)^2 = 4 e / (1 + e)^2
+template <bool BF>
 __device__ __forceinline__ float tanh_slope(float u) {
+  if constexpr (BF) {
+    const float r = tanh_part(u);
+    return __builtin_fmaf(-4.f * r, r, 4.f * r);
+  }
   const float e = exp_of<false>(-2.f * __builtin_fabsf(u)), r = __builtin_amdgcn_rcpf(1.f + e);
   return 4.f * e * r * r;
 }

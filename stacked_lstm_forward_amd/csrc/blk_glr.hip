@@ -400,7 +400,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void glr_bwd_kernel(GlrParams p, lo
     // than a register held.
     float a[NS][V], s[NS][V], up[NS][V], was[NS][V], tz[TANH ? NS : 1][V];
     auto z = [&](int j, int i) {
-      if constexpr (TANH) return BF ? tanh_from(tz[j][i]) : tz[j][i];
+      if constexpr (TANH) return tz[j][i];
       const float v = ru[j].get(i);
       return FULL || t0 + j < n ? v : 0.f;
     };
@@ -416,8 +416,8 @@ __global__ __launch_bounds__(64 * kWaves, 4) void glr_bwd_kernel(GlrParams p, lo
         a[j][i] = in ? g.open : 1.f, s[j][i] = in ? g.shut : 0.f;
         if constexpr (TANH) {
           const float v = ru[j].get(i);
-          tz[j][i] = BF ? tanh_part(v) : tanh_of<false>(v);
-          if (!in) tz[j][i] = BF ? 0.5f : 0.f;  // (a z of 0)
+          tz[j][i] = tanh_of<BF>(v);
+          if (!in) tz[j][i] = 0.f;
         }
         up[j][i] = rd[j].get(i);
         if constexpr (GATE) up[j][i] *= sigmoid_of<BF>(ro[j].get(i));
@@ -485,8 +485,9 @@ __global__ __launch_bounds__(64 * kWaves, 4) void glr_bwd_kernel(GlrParams p, lo
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
       if constexpr (GATE) ro[j].hide();
-      if constexpr (TANH && !BF) ru[j].hide();
+      if constexpr (TANH) ru[j].hide();
     }
+    // (what is made of a candidate is made again, not held)
     auto hide = [&]() {
       if constexpr (TANH && BF)
 #pragma unroll
@@ -522,8 +523,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void glr_bwd_kernel(GlrParams p, lo
         vu[i] = d[i] * s[j][i];
         d[i] *= a[j][i];
         vf[i] = d[i] * ((c[i] - z(j, i)) * s[j][i]);
-        if constexpr (TANH && BF) vu[i] *= slope_from(tz[j][i]);
-        if constexpr (TANH && !BF) vu[i] *= FULL || t0 + j < n ? tanh_slope(ru[j].get(i)) : 0.f;
+        if constexpr (TANH) vu[i] *= FULL || t0 + j < n ? tanh_slope<BF>(ru[j].get(i)) : 0.f;
       }
       if (FULL || t0 + j < p.T) {
         Raw<GBF, V> out;
