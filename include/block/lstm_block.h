@@ -28,7 +28,11 @@
  *     dx = rstd (g - sum g / N - n sum(g n) / N) + ds        (ds NULL: 0)
  *     dw = sum dy n ,  db = sum dy           over all steps of all sentences
  * ds is the gradient that reaches s past the norm; dx is the gradient of x and
- * of r alike.  mean, rstd [B][T] fp32.
+ * of r alike.  mean, rstd [B][T] fp32.  The mean is rounded to fp32 before it is
+ * subtracted (twice at widths above 1024), so a row whose spread is not much more
+ * than 2^-24 of its mean is normalised as accurately as that; rows of one value give
+ * y = b.  Sums and squares are fp32: values' sums have to stay below 2^128, and so
+ * do those of their squared distances to the mean.
  *
  * ---- gated linear recurrence ----------------------------------------------
  * For every channel of every sentence, c_{-1} = c0 (NULL: 0):

@@ -5,8 +5,9 @@
 // walk over rows, forwards with the next row's loads under way; weight and bias
 // stay in registers.  mean and the sum of squares about it take one meeting of the
 // group's waves: each wave takes both about its own mean, and the waves' are joined
-// by their counts (Chan, Golub and LeVeque, 1979), so nothing cancels.  The
-// gradients' two sums meet the same way; dw and db are summed over a workgroup's
+// by their counts (Chan, Golub and LeVeque, 1979), so nothing cancels; a mean of fp32
+// values is corrected by the mean distance to it, which leaves one rounding (0 to 1 %
+// of the passes' time).  The gradients' two sums meet the same way; dw and db are summed over a workgroup's
 // rows in registers, and the workgroups' sums by a second launch, all in a fixed
 // order.
 // Bound by memory where rows are many: 8 x 4096 rows of 4096 (bf16, residual) take
@@ -147,7 +148,20 @@ __global__ __launch_bounds__(threads_of(TPR)) void norm_fwd_kernel(NormParams p)
 #pragma unroll
       for (int i = 0; i < V; ++i) s1 += at.own(k, i) ? sum[k].get(i) : 0.f;
     float mean = lane_sum<kLanes>(s1);
-    mean = mine > 0.f ? mean / mine : 0.f;  // (divided: the mean of equal values is exact)
+    mean = mine > 0.f ? mean / mine : 0.f;
+    // The long sum's roundings, which may be far more than the values' spread, show in the distances to it.  (Not of
+    // bf16 values: where they lie within a factor of 4, the sums of 2^14 of them have 24 bits and are exact; where they
+    // do not, the spread is at least 2^-8 of the largest.)
+    if constexpr (!BF) {
+      float off = 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) off += at.own(k, i) ? sum[k].get(i) - mean : 0.f;
+      off = lane_sum<kLanes>(off);
+      off = mine > 0.f ? off / mine : 0.f;  // (divided: the mean of equal distances is exact, and so that of equal values)
+      if (__builtin_fabsf(off) < __builtin_inff()) mean += off;
+    }
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -159,9 +173,11 @@ __global__ __launch_bounds__(threads_of(TPR)) void norm_fwd_kernel(NormParams p)
     if constexpr (kWaves > 1) {
       if (threadIdx.x % 64 == 0) part[buffer][threadIdx.x / 64] = make_float2(mean, s2);
       __syncthreads();
-      // lane l of every wave joins part l % kWaves
+      // lane l of every wave joins part l % kWaves: the mean by its distance to the first wave's, which has columns
       const float2 o = part[buffer][threadIdx.x % kWaves];
-      mean = lane_sum<kWaves>(other * o.x) / p.N;
+      const float base = part[buffer][0].x;
+      mean = base + lane_sum<kWaves>(other * (o.x - base)) / p.N;
+      if (!(__builtin_fabsf(mean) < __builtin_inff())) mean = lane_sum<kWaves>(other * o.x) / p.N;
       const float d = o.x - mean;
       s2 = lane_sum<kWaves>(other * d * d + o.y);
     }
