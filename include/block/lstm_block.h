@@ -49,6 +49,10 @@
  * fp32's relative accuracy (but not below 2^-126), so gates that are almost shut
  * or open keep theirs.  An infinity or NaN in u or f reaches later steps as
  * infinity or NaN.
+ * A sentence's stretches of steps are worked on side by side and wait for one
+ * another's states.  Every wait ends by itself; one that passes wait_timeout_us all
+ * the same leaves NaN in what depends on it, and lstm_glr_last_error reports it (the
+ * call does not sync).
  *
  * ---- clipping -------------------------------------------------------------
  *     norm = sqrt(sum over all tensors of x^2) ,  coef = min(1, max_norm / (norm + eps))
@@ -122,6 +126,10 @@ typedef struct {
   int32_t cand;                         /* lstm_glr_cand_t: what z is of u */
   lstm_seq_stride_t f, u, o, y;         /* o with an output gate only */
   lstm_seq_stride_t dy, df, du, dout_o; /* lstm_glr_bwd only; dout_o: of do */
+  int64_t wait_timeout_us;              /* limit of a wait for the state before a stretch of steps, in
+                                           microseconds of the kernel's own running; 0 selects the default
+                                           (2 s); negative makes every wait that is not already satisfied
+                                           fail at once (exercises the timeout path without waiting) */
 } lstm_glr_desc_t;
 
 lstm_status_t lstm_glr_validate(const lstm_glr_desc_t *d, int train);
@@ -142,6 +150,13 @@ lstm_status_t lstm_glr_fwd(const lstm_glr_desc_t *d, const void *f, const void *
 lstm_status_t lstm_glr_bwd(const lstm_glr_desc_t *d, const void *f, const void *u, const void *o, const float *c0,
                            const int32_t *lengths, const void *reserve, const void *dy, const float *dcT, void *df,
                            void *du, void *dout_o, float *dc0, void *ws, hipStream_t stream);
+
+/*
+ * Waits for `stream`, then reads the error word that the last lstm_glr_fwd
+ * (train = 0) or lstm_glr_bwd (train = 1) of this description left in `ws`, if it
+ * was the last call on it: LSTM_OK or LSTM_ERR_BARRIER_TIMEOUT.
+ */
+lstm_status_t lstm_glr_last_error(const lstm_glr_desc_t *d, int train, const void *ws, hipStream_t stream);
 
 /* One tensor: `count` contiguous elements. */
 typedef struct {

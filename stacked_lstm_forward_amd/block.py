@@ -10,6 +10,7 @@ Binding (argument marshalling only) under the C names,
     lstm_norm_bwd(desc, s, w, lengths, mean, rstd, dy, ds, dx, dw, db, ws, stream=None) -> status
     lstm_glr_fwd(desc, f, u, o, c0, lengths, y, cT, reserve, ws, stream=None) -> status
     lstm_glr_bwd(desc, f, u, o, c0, lengths, reserve, dy, dcT, df, du, dout_o, dc0, ws, stream=None) -> status
+    lstm_glr_last_error(desc, train, ws, stream=None) -> status
     lstm_clip_table_size(tensors, n) -> int
     lstm_clip_table(tensors, n, table, stream=None) -> status
     lstm_clip(tensors, n, table, max_norm, eps, out, stream=None) -> status
@@ -34,8 +35,8 @@ from . import LSTM_BF16, LSTM_F32, LSTM_OK, _ptr, _stream, check, load_library
 from .decoder import _dtype, _like, _on, _Problem, _ref, _workspace
 
 EXPORTED = ("lstm_norm_validate", "lstm_norm_bwd_workspace_size", "lstm_norm_fwd", "lstm_norm_bwd",
-            "lstm_glr_validate", "lstm_glr_reserve_size", "lstm_glr_workspace_size", "lstm_glr_fwd", "lstm_glr_bwd", "lstm_clip_table_size",
-            "lstm_clip_table", "lstm_clip")
+            "lstm_glr_validate", "lstm_glr_reserve_size", "lstm_glr_workspace_size", "lstm_glr_fwd", "lstm_glr_bwd",
+            "lstm_glr_last_error", "lstm_clip_table_size", "lstm_clip_table", "lstm_clip")
 LSTM_GLR_LINEAR, LSTM_GLR_TANH = 0, 1
 
 
@@ -50,7 +51,7 @@ class NormDesc(ctypes.Structure):
 
 class GlrDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "H", "dtype", "grad_dtype", "cand")] + [
-        (n, SeqStride) for n in ("f", "u", "o", "y", "dy", "df", "du", "dout_o")]
+        (n, SeqStride) for n in ("f", "u", "o", "y", "dy", "df", "du", "dout_o")] + [("wait_timeout_us", ctypes.c_int64)]
 
 
 class ClipTensor(ctypes.Structure):
@@ -73,6 +74,7 @@ def _lib() -> ctypes.CDLL:
                                 ("lstm_norm_bwd", i32, [pn] + [vp] * 12),
                                 ("lstm_glr_validate", i32, [pg, ctypes.c_int]), ("lstm_glr_reserve_size", sz, [pg]), ("lstm_glr_workspace_size", sz, [pg]),
                                 ("lstm_glr_fwd", i32, [pg] + [vp] * 10), ("lstm_glr_bwd", i32, [pg] + [vp] * 14),
+                                ("lstm_glr_last_error", i32, [pg, ctypes.c_int, vp, vp]),
                                 ("lstm_clip_table_size", sz, [pc, i32]), ("lstm_clip_table", i32, [pc, i32, vp, vp]),
                                 ("lstm_clip", i32, [pc, i32, vp, f64, f64, vp, vp])):
         f = getattr(lib, name)
@@ -120,6 +122,10 @@ def lstm_glr_bwd(desc, f, u, o, c0, lengths, reserve, dy, dcT, df, du, dout_o, d
     return int(_lib().lstm_glr_bwd(_ref(desc), _ptr(f), _ptr(u), _ptr(o), _ptr(c0), _ptr(lengths), _ptr(reserve),
                                    _ptr(dy), _ptr(dcT), _ptr(df), _ptr(du), _ptr(dout_o), _ptr(dc0), _ptr(ws),
                                    _stream(stream)))
+
+
+def lstm_glr_last_error(desc, train, ws, stream=None) -> int:
+    return int(_lib().lstm_glr_last_error(_ref(desc), int(train), _ptr(ws), _stream(stream)))
 
 
 def lstm_clip_table_size(tensors, n) -> int:
@@ -385,6 +391,13 @@ class GlrProblem(_SeqProblem):
                                  self.ws.data_ptr(), _on(stream, self.f))
         if st != LSTM_OK:
             check(st, "lstm_glr_bwd")
+
+    def last_error(self, train=False, stream=None) -> int:
+        """The status that the last forward() (train: backward()), if it was the last call, left on the device:
+        LSTM_OK, or LSTM_ERR_BARRIER_TIMEOUT where a wait passed desc.wait_timeout_us.  Waits for the stream."""
+        if not self.gpu:
+            self._runs_on(self.device)
+        return lstm_glr_last_error(self.desc, train, self.ws, _on(stream, self.f))
 
     def advance(self) -> None:
         """Makes the states after this call the next call's first ones (serving: the next step or stretch of

@@ -18,6 +18,7 @@ constexpr long long kMaxCount = (1ll << 31) - 65536;
 constexpr int kMaxNorm = 16384;
 constexpr long long kMaxElements = 1ll << 42;
 constexpr int kMaxTensors = 1 << 20;
+constexpr long long kWait = 2000000, kLongest = 1ll << 50;  // microseconds
 
 bool aligned(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool ws_ok(const void* ws) { return ws && aligned(ws, 256); }
@@ -91,6 +92,8 @@ GlrParams glr_params(const lstm_glr_desc_t* d) {
   p.B = d->B, p.T = d->T, p.H = d->H, p.tanh = d->cand == LSTM_GLR_TANH;
   p.sf = stride(d->f), p.su = stride(d->u), p.so = stride(d->o), p.sy = stride(d->y);
   p.sdy = stride(d->dy), p.sdf = stride(d->df), p.sdu = stride(d->du), p.sdo = stride(d->dout_o);
+  const long long us = d->wait_timeout_us ? d->wait_timeout_us : kWait;
+  p.wait = us < 0 ? -1 : us < kLongest ? us * 100 : kLongest * 100;
   return p;
 }
 
@@ -222,6 +225,17 @@ lstm_status_t lstm_glr_bwd(const lstm_glr_desc_t* d, const void* f, const void* 
   p.dy = dy, p.dcT = dcT, p.df = df, p.du = du, p.dout_o = dout_o, p.dc0 = dc0, p.ws = ws;
   return glr_bwd_launch(p, d->dtype == LSTM_BF16, d->grad_dtype == LSTM_BF16, stream) == hipSuccess ? LSTM_OK
                                                                                                     : LSTM_ERR_HIP;
+}
+
+lstm_status_t lstm_glr_last_error(const lstm_glr_desc_t* d, int train, const void* ws, hipStream_t stream) {
+  const lstm_status_t st = check_glr(d, train != 0);
+  if (st != LSTM_OK) return st;
+  if (!ws_ok(ws)) return LSTM_ERR_WORKSPACE;
+  if (hipStreamSynchronize(stream) != hipSuccess) return LSTM_ERR_HIP;
+  if (!glr_waits(glr_params(d), d->dtype == LSTM_BF16, train != 0)) return LSTM_OK;
+  uint32_t v = 0;
+  if (hipMemcpy(&v, ws, sizeof(v), hipMemcpyDeviceToHost) != hipSuccess) return LSTM_ERR_HIP;
+  return v == 0 ? LSTM_OK : LSTM_ERR_BARRIER_TIMEOUT;
 }
 
 size_t lstm_clip_table_size(const lstm_clip_tensor_t* tensors, int32_t n) {

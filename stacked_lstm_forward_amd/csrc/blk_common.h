@@ -39,6 +39,7 @@ struct GlrParams {
   SeqStride sf, su, so, sy, sdy, sdf, sdu, sdo;
   int B, T, H;
   int tanh;
+  long long wait;  // a wait's limit, ticks of 10 ns
 };
 
 hipError_t norm_fwd_launch(const NormParams& p, bool bf16, hipStream_t stream);
@@ -48,6 +49,7 @@ hipError_t glr_fwd_launch(const GlrParams& p, bool bf16, hipStream_t stream);
 hipError_t glr_bwd_launch(const GlrParams& p, bool bf16, bool grad_bf16, hipStream_t stream);
 size_t glr_reserve(const GlrParams& p, bool bf16);  // floats
 size_t glr_workspace(const GlrParams& p, bool bf16);  // bytes
+bool glr_waits(const GlrParams& p, bool bf16, bool train);  // the workspace begins with an error word
 
 // Steps of sentence b that are its own.
 __device__ __forceinline__ int steps_of(const int32_t* lengths, int b, int T) {

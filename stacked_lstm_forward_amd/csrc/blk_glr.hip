@@ -73,15 +73,20 @@ Plan bwd_plan(const GlrParams& p, bool bf16) { return plan_of(p, bwd_vector(p, b
 // caches in one piece, so nothing else has to be ordered: A with its sign set beside G, or the sign
 // beside the state; 0 is what has not been published.  The workgroups of a sentence's tile take its
 // chunks by a ticket, earlier chunks first: whoever is waited for has started before, and itself
-// waits for none that started later, so every wait ends.  (One that lasts two seconds gives NaN.)
+// waits for none that started later, so every wait ends.  (One that passes the caller's limit gives
+// NaN and sets the error word.  A poll counts for a millisecond at most: a process whose turn on the
+// device is over for longer has not waited.)
 // A ticket for each tile, since one counter for all serves a workgroup every 11 ns.
 constexpr int kGroup = 8;
 static_assert(kGroup == kWaves, "a wave for each chunk of a group");
 struct Chain {
+  uint32_t* error;   // (in a line of its own)
   uint32_t* ticket;  // [B][tiles]
   uint64_t* word;    // [parts][B][tiles][CH]
-  int parts;         // 1: nothing to wait for, no ticket
+  int parts;         // 1: nothing to wait for, none of the above
+  long long limit;   // of a wait, ticks of 10 ns
 };
+constexpr long long kPoll = 100000;  // a millisecond
 
 __global__ __launch_bounds__(256) void glr_clear_kernel(ulonglong2* p, long long n) {
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) p[i] = make_ulonglong2(0, 0);
@@ -102,15 +107,20 @@ __device__ __forceinline__ void chain_state(uint64_t* w, int i, float c) {
 // (a chunk that waits has kWaves = kGroup waves).  `before` is the word of the chunk before, `back` from
 // one to the one before it.
 template <int CH>
-__device__ __forceinline__ void chain_gather(const uint64_t* before, long long back, int i, Map (&lds)[kGroup][CH]) {
+__device__ __forceinline__ void chain_gather(const Chain& chain, const uint64_t* before, long long back, int i,
+                                             Map (&lds)[kGroup][CH]) {
   static_assert(CH <= 64, "a lane for each channel");
   const int q = threadIdx.x >> 6, j = threadIdx.x & 63, words = i % kGroup + (i >= kGroup);
   if (j < CH && q < words) {
     const uint64_t* w = before + q * back + j;
-    const long long begin = wall_clock64();
+    long long last = wall_clock64(), waited = 0;
     uint64_t v;
     while (!(v = __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))) {
-      if (wall_clock64() - begin > 200000000ll) {  // (ticks of 10 ns)
+      const long long now = wall_clock64(), since = now - last;
+      last = now;
+      waited += since < kPoll ? since : kPoll;
+      if (waited > chain.limit) {
+        __hip_atomic_store(chain.error, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         v = 0x7fc000007fc00000ull;
         break;
       }
@@ -270,7 +280,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void glr_fwd_kernel(GlrParams p, lo
         for (int w = 1; w < waves; ++w) m = map_join(total[w][threadIdx.x], m);
         chain_map(word + threadIdx.x, part, m);
       }
-      chain_gather(word - word_step, -word_step, part, words);
+      chain_gather(chain, word - word_step, -word_step, part, words);
     }
     for (int j = threadIdx.x; j < CH; j += blockDim.x) {
       float c = p.c0 ? p.c0[at.state(p, j)] : 0.f;
@@ -462,7 +472,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void glr_bwd_kernel(GlrParams p, lo
         for (int w = waves - 2; w >= 0; --w) m = map_join({total[w][threadIdx.x].A, total_g[w][threadIdx.x]}, m);
         chain_map(word + threadIdx.x, i, m);
       }
-      chain_gather(word + word_step, word_step, i, words);
+      chain_gather(chain, word + word_step, word_step, i, words);
     }
     for (int j = threadIdx.x; j < CH; j += blockDim.x) {
       float c = p.reserve[(long long)part * p.B * p.H + at.state(p, j)];
@@ -549,19 +559,21 @@ __global__ __launch_bounds__(64 * kWaves, 4) void glr_bwd_kernel(GlrParams p, lo
     step(No());
 }
 
-// The chain's 64-bit words: of the tickets (in lines of their own), and of the chunks.
-long long ticket_words(const GlrParams& p, const Plan& s) { return (p.B * s.tiles + 63) / 64 * 32; }
+// The chain's 64-bit words: of the error word and the tickets (in lines of their own), and of the chunks.
+constexpr int kErrorWords = 32;
+long long ticket_words(const GlrParams& p, const Plan& s) { return kErrorWords + (p.B * s.tiles + 63) / 64 * 32; }
 long long chain_words(const GlrParams& p, const Plan& s, int V) {
   return s.parts > 1 ? ticket_words(p, s) + s.parts * p.B * s.tiles * s.cw * V : 0;
 }
 
-// The chain's ticket and words, cleared.
+// The chain's error word, tickets and words, cleared.
 Chain chain_of(const GlrParams& p, const Plan& s, int V, hipStream_t stream) {
   if (s.parts > 1) {
     const long long n = chain_words(p, s, V) / 2;  // (a tile has an even number of channels)
     glr_clear_kernel<<<(int)(n / 256 < 1024 ? n / 256 + 1 : 1024), 256, 0, stream>>>((ulonglong2*)p.ws, n);
   }
-  return Chain{(uint32_t*)p.ws, (uint64_t*)p.ws + ticket_words(p, s), s.parts};
+  uint64_t* w = (uint64_t*)p.ws;
+  return Chain{(uint32_t*)w, (uint32_t*)(w + kErrorWords), w + ticket_words(p, s), s.parts, p.wait};
 }
 
 template <bool BF, int V, bool GATE>
@@ -602,6 +614,10 @@ size_t glr_workspace(const GlrParams& p, bool bf16) {
   const long long f = chain_words(p, fwd_plan(p, bf16), fwd_vector(p, bf16));
   const long long b = chain_words(p, bwd_plan(p, bf16), bwd_vector(p, bf16));
   return 8 * (size_t)(f > b ? f : b) + 256;
+}
+
+bool glr_waits(const GlrParams& p, bool bf16, bool train) {
+  return train ? bwd_plan(p, bf16).parts > 1 : fwd_plan(p, bf16).parts > 1;
 }
 
 hipError_t glr_fwd_launch(const GlrParams& p, bool bf16, hipStream_t stream) {
