@@ -24,7 +24,9 @@ and on top of it problems that own outputs and workspaces, made once per shape:
     p = prepare_clip(gradients, max_norm=1.0);  p.run()       # p.norm, p.coef, the gradients
 
 Problems read their tensors as those of ``decoder.py`` do: whatever they hold at
-the call, and what replaces one is checked like the first.
+the call, and what replaces one (``p.x = t``) is checked like the first.  The tensors
+themselves keep their shape, strides and type; those of a clipping problem may be
+given other memory (``t.data = ..``) and are looked at before every call.
 """
 from __future__ import annotations
 
@@ -33,6 +35,7 @@ from dataclasses import dataclass
 
 from . import LSTM_BF16, LSTM_F32, LSTM_OK, _ptr, _stream, check, load_library
 from .decoder import _dtype, _like, _on, _Problem, _ref, _workspace
+from .held import Held
 
 EXPORTED = ("lstm_norm_validate", "lstm_norm_bwd_workspace_size", "lstm_norm_fwd", "lstm_norm_bwd",
             "lstm_glr_validate", "lstm_glr_reserve_size", "lstm_glr_workspace_size", "lstm_glr_fwd", "lstm_glr_bwd",
@@ -461,7 +464,7 @@ class ClipProblem:
         import torch
         self.tensors, self.out = tuple(tensors), tuple(out)
         self.max_norm, self.eps = max_norm, eps
-        self._all, self._address = self.tensors + self.out, torch.Tensor.data_ptr
+        self._all = self.tensors + self.out
         n = len(self.tensors)
         if n == 0 or len(self.out) != n:
             raise ValueError(f"{n} tensors and {len(self.out)} outputs: one tensor at least, and an output for each")
@@ -474,7 +477,8 @@ class ClipProblem:
                 raise ValueError(f"tensor {i}: on {t.device}, expected {self.device}")
             _like(x, f"output {i}", t.shape, t.dtype, self.device)
             self._list[i].count, self._list[i].dtype = t.numel(), _dtype(t, f"tensor {i}")
-        self._point(self._addresses())
+        self._held = Held(self._all)
+        self._point()
         size = lstm_clip_table_size(self._list, n)
         if size == 0:
             raise ValueError("unsupported tensors: lstm_clip_table_size returned 0")
@@ -484,11 +488,8 @@ class ClipProblem:
         self._result = torch.empty(2, dtype=torch.float32, device=self.device)
         self.norm, self.coef = self._result[0], self._result[1]
 
-    def _addresses(self):
-        return list(map(self._address, self._all))
-
-    def _point(self, at) -> None:
-        n = len(self.tensors)
+    def _point(self) -> None:
+        n, at = len(self.tensors), [t.data_ptr() for t in self._all]
         # an output may be its own tensor, and nothing else that is read or written
         spans = []
         for i, (t, src, dst) in enumerate(zip(self.tensors, at[:n], at[n:])):
@@ -502,24 +503,31 @@ class ClipProblem:
             written = max(written, hi) if out else written
         for e, src, dst in zip(self._list, at[:n], at[n:]):
             e.src, e.dst = src, dst
-        self._at = at
+
+    def _moved(self) -> bool:
+        """Whether a tensor was given other memory since the last call, which the entries then point to.  Another
+        size, type, device or order of its values is refused, at the same address too."""
+        if self._held.same():
+            return False
+        n = len(self.tensors)
+        for i, t in enumerate(self._all):
+            e = self._list[i % n]
+            if (t.numel() != e.count or t.device != self.device or not t.is_contiguous() or
+                    _dtype(t, f"tensor {i % n}") != e.dtype):
+                raise ValueError(f"{'tensor' if i < n else 'output'} {i % n}: no longer what the problem was made for")
+        self._point()
+        self._held.read()
+        return True
 
     def run(self, stream=None) -> None:
         """norm, coef, and every output = coef * its tensor."""
         import torch
+        if self._moved():
+            self._written = None
         if self.device.type != "cuda":
             raise ValueError(f"the problem's tensors are on {self.device}: the kernels run on a GPU")
         s = _on(stream, self._result)
         lib, n, table = _lib(), len(self.tensors), self._table.data_ptr()
-        at = self._addresses()
-        if at != self._at:  # (a tensor was given other memory)
-            for i, t in enumerate(self._all):
-                e = self._list[i % n]
-                if (t.numel() != e.count or t.device != self.device or not t.is_contiguous() or
-                        _dtype(t, f"tensor {i % n}") != e.dtype):
-                    raise ValueError(f"tensor {i % n}: no longer what the problem was made for")
-            self._point(at)
-            self._written = None
         # the table is written once for the current stream; a captured call, and one on a stream that may be
         # captured, writes its own, and so does every call after it
         if stream is not None or torch.cuda.is_current_stream_capturing():

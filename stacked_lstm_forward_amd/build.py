@@ -1,7 +1,11 @@
-"""Builds the gfx950 shared libraries in-tree with hipcc:
+"""Builds the shared libraries in-tree, for gfx950 with hipcc:
 
     lib/liblstm_fwd.so    the forward pass (include/lstm_fwd.h)
     lib/liblstm_peaks.so  the measured-peak microbenchmarks (include/lstm_peaks.h)
+
+and for the host with the C++ compiler, against the installed torch:
+
+    lib/liblstm_held.so   reads what lists of tensors are (held.py)
 
     python -m stacked_lstm_forward_amd.build
 """
@@ -17,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "liblstm_fwd.so")
 PEAKS_LIB = os.path.join(LIBDIR, "liblstm_peaks.so")
+HELD_LIB = os.path.join(LIBDIR, "liblstm_held.so")
 ARCH = "gfx950"
 # (source, extra defines): the recurrent kernel is instantiated once per
 # (dtype, weight source, waves per workgroup) so the variants compile in parallel
@@ -50,6 +55,21 @@ def _flags() -> list:
             "-I", os.path.join(os.path.dirname(HERE), "include")]
 
 
+def _held_command() -> list:
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    cc = shutil.which("g++") or shutil.which("c++")
+    if cc is None:
+        raise RuntimeError("no C++ compiler found")
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [cc, "-O2", "-std=c++17", "-shared", "-fPIC",
+            *[x for p in (*include_paths(), sysconfig.get_paths()["include"]) for x in ("-isystem", p)],
+            os.path.join(CSRC, "torch_held.cpp"), "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-o", HELD_LIB + ".tmp"]
+
+
 def build(verbose: bool = False) -> str:
     from concurrent.futures import ThreadPoolExecutor
 
@@ -61,6 +81,7 @@ def build(verbose: bool = False) -> str:
         for i, (src, defs) in enumerate(units):
             obj = os.path.join(BUILD_DIR, f"{tag}_{i:02d}_{os.path.splitext(src)[0]}.o")
             jobs.append((tag, obj, [cc, *_flags(), *defs, "-c", os.path.join(CSRC, src), "-o", obj]))
+    jobs.append(("held", HELD_LIB + ".tmp", _held_command()))
 
     def run(job):
         _, obj, cmd = job
@@ -68,7 +89,7 @@ def build(verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"hipcc failed ({r.returncode}): {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"compiler failed ({r.returncode}): {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return obj
 
     workers = max(1, min(len(jobs), os.cpu_count() or 1, 8))
@@ -84,6 +105,7 @@ def build(verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
+    os.replace(HELD_LIB + ".tmp", HELD_LIB)
     return LIB
 
 
