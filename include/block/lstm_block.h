@@ -59,7 +59,7 @@
  *     dst = coef src       for every tensor (a NULL dst is left out of this)
  * dst may be src.  Sums are taken in 64 bits, so no square overflows; a NaN makes
  * coef NaN, an infinity makes it 0, as the formula says.  With an infinite max_norm
- * coef is 1 whatever the norm.  out holds norm and coef.
+ * coef is 1 whatever the norm, and where norm + eps is 0.  out holds norm and coef.
  *
  * ---- all ------------------------------------------------------------------
  * dtype is an lstm_dtype_t; arithmetic and statistics are fp32 or wider, each

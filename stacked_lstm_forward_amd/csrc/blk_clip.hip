@@ -137,7 +137,8 @@ __global__ __launch_bounds__(256) void clip_scale_kernel(ClipParams p) {
   const long long from = clip_from(p.chunks, p.blocks, blockIdx.x), to = clip_from(p.chunks, p.blocks, blockIdx.x + 1);
   double sum = 0;
   for (int i = threadIdx.x; i < p.blocks; i += 256) sum += p.part[i];
-  const double norm = sqrt(block_sum(sum, lds)), c = isinf(p.max_norm) ? 1. : p.max_norm / (norm + p.eps);
+  const double norm = sqrt(block_sum(sum, lds)), by = norm + p.eps;
+  const double c = isinf(p.max_norm) || by == 0. ? 1. : p.max_norm / by;  // (no 0 / 0)
   const double coef = c > 1. ? 1. : c;  // (in 64 bits for the products too: it may be small)
   if (blockIdx.x == 0 && threadIdx.x == 0) p.out[0] = (float)norm, p.out[1] = (float)coef;
   if (from >= to) return;
