@@ -92,3 +92,17 @@ def test_glr_small_candidates(T, by, types):
     # the slope: in fp32 4 e / (1 + e)^2 with 15 W (e's 3 twice, and 9), in bf16 a rounding; and u^2, 4 W
     value, bound = want["du"]
     within(p.du, (value, bound + 20 * W * most["du"][0]), "du")
+
+
+@pytest.mark.parametrize("T", [1, 3, 600])
+def test_glr_tanh_of_fp32_values(T):
+    """(1 - e) / (1 + e): 6 W, and e's 3 W times 2 e / (1 - e^2) < 2 from 1/4 on; the series below less than 6 W; the
+    gate that is shut and its product 5 W."""
+    g = torch.Generator().manual_seed(T)
+    last = torch.cat([torch.randn(50, 1, 64, generator=g) * 10.0 ** k for k in range(-20, 2)])
+    u = torch.zeros(last.shape[0], T, 64)
+    u[:, -1:] = last
+    p = block.prepare_glr(torch.full_like(u, -math.inf).to(DEV), u.to(DEV), tanh=True)
+    p.forward()
+    z = torch.tanh(last[:, 0].double())
+    within(p.cT, (z, 17 * W * z.abs()), "tanh")
