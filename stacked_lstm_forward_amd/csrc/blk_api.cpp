@@ -13,7 +13,8 @@ using namespace lstm;
 
 namespace {
 
-// Counts are held in 32 bits, and the kernels' counters step past them by less than 65536.
+// Counts are held in 32 bits, and the kernels' signed counters step past them by less than 65536 (the recurrence's by
+// a chunk of 512 steps at the most).  The norm's rows, which step by up to 6 x 256 x 64, are counted without a sign.
 constexpr long long kMaxCount = (1ll << 31) - 65536;
 constexpr int kMaxNorm = 16384;
 constexpr long long kMaxElements = 1ll << 42;

@@ -13,9 +13,10 @@
 // states forwards, from the one that the forward kept for the chunk, the carry
 // backwards.
 // Bound by memory, beside a vector pipe at 70 % (forwards) and 54 %: 4 x 16384 x 1536
-// (bf16, output gate) 165 us forwards and 298 backwards, 4.9 and 4.8 TB/s; single
-// steps by the launch (16 x 4096: 5.1 us), short sequences by loads, scan and stores
-// after each other (64 x 100 x 512, fp32: 11 and 15 us).
+// (bf16, output gate) 469 us forwards and backwards, 4.8 TB/s (passes after each other; a
+// kernel trace, which parts them, has 170 and 318, and 5 each to clear the chain's words);
+// single steps by the launch (16 x 4096: 5.1 us), short sequences by loads, scan and
+// stores after each other (64 x 100 x 512, fp32: 11 and 15 us).
 #include "blk_common.h"
 #include "blk_gate.h"
 
@@ -37,8 +38,10 @@ struct Plan {
 };
 
 // Channels of a lane: 8 bytes' worth forwards, two backwards, which has more to hold of each, and one in fp32 where
-// the sequence is long: with two, gates and tanh spill (32 x 500 x 4096: 437 us for 393, with tanh 528 for 420), with
-// one, short sequences have fewer slots in a wave (64 x 100 x 512: 18.6 us for 16.0).  One where there are fewer.
+// the sequence is long: with two, gates and tanh spill, 7 registers with an output gate, 38 with both (32 x 500 x 4096:
+// 437 us for 393, with tanh 528 for 420), with one, short sequences have fewer slots in a wave (64 x 100 x 512 without
+// an output gate: 18.6 us for 16.0; between 100 and 500 steps, and short ones with gate and tanh, neither was measured).
+// One where there are fewer.
 int fwd_vector(const GlrParams& p, bool bf16) { return bf16 && p.H >= 4 ? 4 : !bf16 && p.H >= 2 ? 2 : 1; }
 int bwd_vector(const GlrParams& p, bool bf16) { return p.H >= 2 && (bf16 || p.T <= 256) ? 2 : 1; }
 constexpr int width_of(int V, int size) { return V * size * 16 >= 128 ? 16 : V * size * 32 >= 128 ? 32 : 64; }

@@ -6,14 +6,15 @@
 // stay in registers.  mean and the sum of squares about it take one meeting of the
 // group's waves: each wave takes both about its own mean, and the waves' are joined
 // by their counts (Chan, Golub and LeVeque, 1979), so nothing cancels; a mean of fp32
-// values is corrected by the mean distance to it, which leaves one rounding (0 to 1 %
-// of the passes' time).  The gradients' two sums meet the same way; dw and db are summed over a workgroup's
+// values is corrected by the mean distance to it, which leaves one rounding (0 to 2 %
+// of the forward's time).  The gradients' two sums meet the same way; dw and db are summed over a workgroup's
 // rows in registers, and the workgroups' sums by a second launch, all in a fixed
 // order.
 // Bound by memory where rows are many: 8 x 4096 rows of 4096 (bf16, residual) take
-// 204 us forwards and 204 backwards with the join, 5.3 TB/s; by launches, loads and
-// meetings after each other where they are few: 16 rows of 4096 5.0 us, 64 x 100
-// rows of 512 (fp32) 11 and 16 us.
+// 413 us forwards and backwards with the join, 5.3 TB/s (passes after each other; a
+// kernel trace, which parts them, has 198, 218 and 5); by launches, loads and meetings
+// after each other where they are few: 16 rows of 4096 5.1 us, 64 x 100 rows of 512
+// (fp32) 27 us (12, 13 and 4).
 #include "blk_common.h"
 
 namespace lstm {
@@ -390,8 +391,10 @@ int blocks_of(const NormParams& p, int per_unit, int least) {
   if (walk < least) walk = least;
   return (int)((n + walk - 1) / walk);
 }
-// What the registers let a compute unit hold, and backwards less: each leaves 2 N sums behind (8 x 4096 rows of
-// 4096: 237 us with four workgroups a compute unit, 222 with three, 204 with two, 270 with one).
+// About what the registers let a compute unit hold (with 8 elements a lane six to eight, with 16 five of bf16 and
+// four of fp32, whose fifth follows the others: 8 x 4096 rows of 4096, fp32, 427 us, 5.0 TB/s), and backwards less:
+// each leaves 2 N sums behind (8 x 4096 rows of 4096: 237 us with four workgroups a compute unit, 222 with three, 204
+// with two, 270 with one).
 int fwd_blocks(const NormParams& p) {
   const Shape s = shape_of(p.N);
   return blocks_of(p, s.tpr > 256 ? 1 : s.e == 8 ? 6 : 5, 1);
